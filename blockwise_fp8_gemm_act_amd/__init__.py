@@ -1,9 +1,9 @@
-"""Python binding of libpuro.so: blockwise-FP8 quantizers and the
-blockwise-scaled FP8 GEMM for MI355X (gfx950).
+"""Python binding of libpuro.so: blockwise-FP8 quantizers, the
+blockwise-scaled FP8 GEMM and the attention block for MI355X (gfx950).
 
 Argument marshalling only.  Every step of the computation runs in the HIP
-kernels behind the C ABI declared in ``include/puro.h``; PyTorch is used for
-device memory and streams.  There is no fallback: if the library is missing,
+kernels behind the C ABI declared in ``include/puro.h`` and
+``include/puro_attention.h``; PyTorch is used for device memory and streams.  There is no fallback: if the library is missing,
 importing this package fails.
 
 The raw C calls keep their C names (``puro_quant_act_1x128``,
@@ -16,6 +16,11 @@ tensor-level helpers ``quant_act_1x128``, ``quant_w_128x128``,
 ``gemm_fp8_blockwise``, ``gemm_fp8_blockwise_accumulate`` and
 ``gemm_fp8_swiglu_quant`` allocate outputs with torch and call them on the
 current stream.
+
+The attention block (``rope_table``, ``rope``, ``qk_norm_rope``,
+``qk_norm_rope_append``, ``qk_norm_rope_backward``, ``attention``,
+``attention_backward`` and their ``puro_`` calls) lives in ``_attention.py`` and is
+re-exported here.
 """
 from __future__ import annotations
 
@@ -31,7 +36,8 @@ LIB_PATH = os.path.join(_HERE, "libpuro.so")
 PURO_OK = 0
 STATUS_NAMES = {0: "PURO_OK", 1: "PURO_ERR_NULL", 2: "PURO_ERR_SHAPE", 3: "PURO_ERR_ALIGN",
                 4: "PURO_ERR_MODE", 5: "PURO_ERR_DTYPE", 6: "PURO_ERR_WORKSPACE",
-                7: "PURO_ERR_DEVICE", 8: "PURO_ERR_LAUNCH", 9: "PURO_ERR_ALIAS", 10: "PURO_ERR_SCRATCH"}
+                7: "PURO_ERR_DEVICE", 8: "PURO_ERR_LAUNCH", 9: "PURO_ERR_ALIAS", 10: "PURO_ERR_SCRATCH",
+                11: "PURO_ERR_VALUE"}
 SCRATCH_BYTES = 64 << 20       # device scratch of puro_gemm_fp8_blockwise_noalloc, per GPU
 FPROP, DGRAD, WGRAD, WGRAD_TM = 0, 1, 2, 3
 OUT_F32, OUT_BF16 = 0, 1
@@ -475,3 +481,11 @@ def gemm_fp8_swiglu_quant(a, sa, b, sb, write_gu: bool = True, stream=None):
                                       gu.data_ptr() if write_gu else None, hq.data_ptr(), hs.data_ptr(),
                                       _stream(stream)), "puro_gemm_fp8_swiglu_quant")
     return hq, hs, gu
+
+
+from ._attention import (  # noqa: E402  (the attention block uses the helpers above)
+    ROPE_HALF, ROPE_INTERLEAVED, ROPE_LINEAR, ROPE_NTK, ROPE_PLAIN, ROPE_YARN, AttentionShape, Rotation, attention,
+    attention_backward, puro_attention, puro_attention_backward, puro_attention_backward_workspace_bytes,
+    puro_attention_workspace_bytes, puro_qk_norm_rope, puro_qk_norm_rope_append, puro_qk_norm_rope_backward,
+    puro_qk_norm_rope_backward_workspace_bytes, puro_rope, puro_rope_table, qk_norm_rope, qk_norm_rope_append,
+    qk_norm_rope_backward, rope, rope_table)

@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libpuro.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
-SOURCES = ["quant.hip", "gemm.hip", "abi.cpp"]
+SOURCES = ["quant.hip", "gemm.hip", "rope.hip", "attention.hip", "attention_backward.hip", "abi.cpp", "abi_attention.cpp"]
 
 # gfx950 only.  Packed fp32 VALU instructions are disabled for all device code.
 HIPCC_FLAGS = [

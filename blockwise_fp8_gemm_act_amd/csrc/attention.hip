@@ -1,0 +1,401 @@
+// Attention forward (gfx950): softmax(scale q k^T + mask) v in one pass over the
+// keys with a running maximum and sum.
+//
+//   attn_kernel        many queries: 256 queries of one head a workgroup, 32 a wave
+//   attn_split_kernel  few queries: 32 (query, head) rows a workgroup, the keys
+//                      dealt over its waves and over `splits` workgroups
+//   attn_join_kernel   joins the splits
+#include "attention_common.h"
+
+namespace puro {
+namespace {
+
+// Scores of 32 keys x 32 queries from a key tile in LDS and the queries' fragments.
+template <int kHd>
+__device__ __forceinline__ f32x16 score_tile(uint32_t ktile, int r0, const bf16x8 *qf) {
+  f32x16 s = {};
+#pragma unroll
+  for (int kk = 0; kk < kHd / 16; ++kk) s = mfma(row_frag<kHd>(ktile, r0, kk), qf[kk], s);
+  return s;
+}
+
+__device__ __forceinline__ void mask_tile(f32x16 &s, int key0, int p, int window, int sinks) {
+  const int half = (threadIdx.x & 63) >> 5;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int key = key0 + 8 * (i / 4) + 4 * half + i % 4;
+    s[i] = visible(key, p, window, sinks) ? s[i] : -__builtin_inff();
+  }
+}
+
+// Softmax state of one query (of a lane and its partner): m is the maximum in use,
+// in units of log2, l this lane's share of the sum.
+template <int kHd>
+struct Row {
+  f32x16 o[kHd / 32];
+  float m, l;
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int d = 0; d < kHd / 32; ++d) o[d] = (f32x16){};
+    m = kNoMax;
+    l = 0.0f;
+  }
+
+  // The maximum in use follows the true one only once that is 2^8 larger: until
+  // then exp2(s - m) stays below 2^8, which costs bf16 no precision, and the
+  // accumulators need no rescaling.
+  __device__ __forceinline__ void raise(float top) {
+    if (__any(top > m + 8.0f)) {
+      const float next = fmaxf(m, top);
+      const float f = __builtin_amdgcn_exp2f(m - next);
+      m = next;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < kHd / 32; ++d) o[d] *= f;
+    }
+  }
+};
+
+__device__ __forceinline__ float tile_max(const f32x16 &s) {
+  float t = s[0];
+#pragma unroll
+  for (int i = 1; i < 16; ++i) t = fmaxf(t, s[i]);
+  return t;
+}
+
+// ---------------------------------------------------------------- many queries
+constexpr int kFwdWaves = 8, kFwdRows = 32 * kFwdWaves, kFwdKeys = 64;
+
+template <int kHd>
+__global__ void __launch_bounds__(64 * kFwdWaves, 2) attn_kernel(AttnArgs a, int slots) {
+  constexpr int kTile = kFwdKeys * kHd;
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[2][2][kTile];
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // Key heads run fastest over the workgroups, so that with 8 of them each XCD's L2
+  // serves one; the last tiles of a sequence, which see most keys, start first.
+  const int hk = (int)(blockIdx.x % a.k_heads);
+  const int rest = (int)(blockIdx.x / a.k_heads);
+  const int h = hk * a.group + rest % a.group;
+  int slot = slots - 1 - rest / a.group;
+  const Seq sq = load_seq(a, find_seq(a.q_start, a.sequences, a.q_tokens, 1, kFwdRows, slot));
+  if ((int64_t)slot * kFwdRows >= sq.ql) return;
+  const int row0 = slot * kFwdRows;
+  const int rows = sq.ql - row0 < kFwdRows ? sq.ql - row0 : kFwdRows;
+  const int shift = sq.kl - sq.ql;                              // position of query 0
+  const KeyTiles kt = key_tiles(shift + row0, shift + row0 + rows - 1, a.window, a.sinks, kFwdKeys);
+
+  const int mine = 32 * wave + (lane & 31);                     // this lane's query in the block
+  const int qrow = sq.q0 + row0 + (mine < rows ? mine : rows - 1);
+  const int p = shift + row0 + mine;
+  const int w_lo = shift + row0 + 32 * wave, w_hi = w_lo + 31;  // positions of the wave's queries
+  bf16x8 qf[kHd / 16];
+#pragma unroll
+  for (int kk = 0; kk < kHd / 16; ++kk)
+    qf[kk] = load8(a.q + (int64_t)qrow * a.qs + (int64_t)h * kHd + 16 * kk + 8 * half);
+
+  const uint16_t *kbase = a.k + (int64_t)sq.k0 * a.ks + (int64_t)hk * kHd;
+  const uint16_t *vbase = a.v + (int64_t)sq.k0 * a.vs + (int64_t)hk * kHd;
+  const uint32_t lds0 = lds_addr(lds);
+  auto copy = [&](int i, int buf) {
+    const int key0 = kt.key0(i, kFwdKeys);
+    const uint32_t at = lds0 + (uint32_t)(buf * 2 * kTile * 2);
+#pragma unroll
+    for (int c = wave; c < kFwdKeys / kDmaRows<kHd>; c += kFwdWaves) {
+      copy_rows<kHd>(at, c * kDmaRows<kHd>, [&](int r) { return kbase + (int64_t)kt.row(key0 + r) * a.ks; });
+      copy_rows<kHd>(at + kTile * 2, c * kDmaRows<kHd>,
+                     [&](int r) { return vbase + (int64_t)kt.row(key0 + r) * a.vs; });
+    }
+  };
+
+  Row<kHd> st;
+  st.clear();
+  const float c2 = a.scale * kLog2e;
+  if (kt.count > 0) copy(0, 0);
+  for (int i = 0; i < kt.count; ++i) {
+    // This tile has landed, and every wave is done with the other buffer.
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (i + 1 < kt.count) copy(i + 1, (i + 1) & 1);
+    const int key0 = kt.key0(i, kFwdKeys);
+    const uint32_t ktile = lds0 + (uint32_t)((i & 1) * 2 * kTile * 2), vtile = ktile + kTile * 2;
+    const bool none = key0 > w_hi || (a.window > 0 && key0 + kFwdKeys - 1 <= w_lo - a.window && key0 >= a.sinks);
+    if (none) continue;
+    const bool all = key0 + kFwdKeys - 1 <= w_lo &&
+                     (a.window == 0 || key0 > w_hi - a.window || key0 + kFwdKeys <= a.sinks);
+    f32x16 s[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      s[b] = score_tile<kHd>(ktile, 32 * b, qf);
+      if (!all) mask_tile(s[b], key0 + 32 * b, p, a.window, a.sinks);
+    }
+    st.raise(half_max(fmaxf(tile_max(s[0]), tile_max(s[1]))) * c2);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        s[b][j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][j], c2, -st.m));
+        st.l += s[b][j];
+      }
+#pragma unroll
+      for (int step = 0; step < 2; ++step) {
+        const bf16x8 pf = pack_step(s[b], step);
+#pragma unroll
+        for (int d = 0; d < kHd / 32; ++d)
+          st.o[d] = mfma(col_frag<kHd>(vtile, 32 * b + 16 * step, d), pf, st.o[d]);
+      }
+    }
+  }
+
+  const float l = half_sum(st.l);
+  if (mine < rows) {
+    const float f = l > 0.0f ? 1.0f / l : 0.0f;
+    uint16_t *orow = a.o + (int64_t)qrow * a.os + (int64_t)h * kHd;
+#pragma unroll
+    for (int d = 0; d < kHd / 32; ++d) store_block(orow + 32 * d, st.o[d], f);
+    if (a.lse && half == 0)
+      a.lse[(int64_t)h * a.q_tokens + qrow] = l > 0.0f ? (st.m + __builtin_log2f(l)) * kLn2 : -__builtin_inff();
+  }
+}
+
+// ---------------------------------------------------------------- few queries
+constexpr int kSplitWaves = 4, kSplitRows = 32, kSplitKeys = 32;
+
+// Partials of one (tile, key head, split): kSplitRows rows of kHd values, then m
+// and l of each row.
+template <int kHd>
+__device__ __host__ constexpr size_t split_floats() {
+  return (size_t)kSplitRows * (kHd + 2);
+}
+
+// A row of a tile is (query, head of the group): rows of a sequence are numbered
+// query * group + head, so that the heads that share keys share the tile.  Each
+// wave keeps its own two stages of keys and values in LDS and waits for nobody;
+// the waves' states are joined at the end.
+template <int kHd>
+__global__ void __launch_bounds__(64 * kSplitWaves) attn_split_kernel(AttnArgs a, int splits) {
+  constexpr int kTile = kSplitKeys * kHd, kStage = 2 * kTile;
+  constexpr int kCopies = kSplitKeys / kDmaRows<kHd>;
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[kSplitWaves][2][kStage];
+  __shared__ float stat[kSplitWaves][2][kSplitRows];
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int hk = (int)(blockIdx.x % a.k_heads);
+  const int rest = (int)(blockIdx.x / a.k_heads);
+  const int split = rest % splits, tile = rest / splits;
+  int slot = tile;
+  const Seq sq = load_seq(a, find_seq(a.q_start, a.sequences, a.q_tokens, a.group, kSplitRows, slot));
+  const int all_rows = sq.ql * a.group;
+  if ((int64_t)slot * kSplitRows >= all_rows) return;
+  const int row0 = slot * kSplitRows;
+  const int rows = all_rows - row0 < kSplitRows ? all_rows - row0 : kSplitRows;
+  const int shift = sq.kl - sq.ql;
+  const KeyTiles kt = key_tiles(shift + row0 / a.group, shift + (row0 + rows - 1) / a.group, a.window, a.sinks, kSplitKeys);
+
+  const int mine = lane & 31;
+  const int r = row0 + (mine < rows ? mine : rows - 1);
+  const int qi = r / a.group, h = hk * a.group + r % a.group;
+  const int qrow = sq.q0 + qi, p = shift + qi;
+  const int p_lo = shift + row0 / a.group, p_hi = shift + (row0 + rows - 1) / a.group;
+  bf16x8 qf[kHd / 16];
+#pragma unroll
+  for (int kk = 0; kk < kHd / 16; ++kk)
+    qf[kk] = load8(a.q + (int64_t)qrow * a.qs + (int64_t)h * kHd + 16 * kk + 8 * half);
+
+  const uint16_t *kbase = a.k + (int64_t)sq.k0 * a.ks + (int64_t)hk * kHd;
+  const uint16_t *vbase = a.v + (int64_t)sq.k0 * a.vs + (int64_t)hk * kHd;
+  const uint32_t lds0 = lds_addr(lds[wave]);
+  auto copy = [&](int i, int buf) {
+    const int key0 = kt.key0(i, kSplitKeys);
+    const uint32_t at = lds0 + (uint32_t)(buf * kStage * 2);
+#pragma unroll
+    for (int c = 0; c < kCopies; ++c)
+      copy_rows<kHd>(at, c * kDmaRows<kHd>, [&](int x) { return kbase + (int64_t)kt.row(key0 + x) * a.ks; });
+#pragma unroll
+    for (int c = 0; c < kCopies; ++c)
+      copy_rows<kHd>(at + kTile * 2, c * kDmaRows<kHd>,
+                     [&](int x) { return vbase + (int64_t)kt.row(key0 + x) * a.vs; });
+  };
+
+  Row<kHd> st;
+  st.clear();
+  const float c2 = a.scale * kLog2e;
+  const int begin = (int)((int64_t)kt.count * split / splits), end = (int)((int64_t)kt.count * (split + 1) / splits);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");    // only copies are counted from here on
+  int i = begin + wave;
+  if (i < end) copy(i, 0);
+  for (int buf = 0; i < end; i += kSplitWaves, buf ^= 1) {
+    // The other buffer's reads are done; once its copies are under way only they may
+    // be outstanding.
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (i + kSplitWaves < end) {
+      copy(i + kSplitWaves, buf ^ 1);
+      if (kCopies == 8) asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
+      else asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+    } else {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+    const int key0 = kt.key0(i, kSplitKeys);
+    const uint32_t ktile = lds0 + (uint32_t)(buf * kStage * 2), vtile = ktile + kTile * 2;
+    const bool all = key0 + kSplitKeys - 1 <= p_lo &&
+                     (a.window == 0 || key0 > p_hi - a.window || key0 + kSplitKeys <= a.sinks);
+    f32x16 s = score_tile<kHd>(ktile, 0, qf);
+    if (!all) mask_tile(s, key0, p, a.window, a.sinks);
+    st.raise(half_max(tile_max(s)) * c2);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      s[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], c2, -st.m));
+      st.l += s[j];
+    }
+#pragma unroll
+    for (int step = 0; step < 2; ++step) {
+      const bf16x8 pf = pack_step(s, step);
+#pragma unroll
+      for (int d = 0; d < kHd / 32; ++d) st.o[d] = mfma(col_frag<kHd>(vtile, 16 * step, d), pf, st.o[d]);
+    }
+  }
+
+  // Join the waves: each scales its state to the common maximum, wave by wave in
+  // order, through LDS (which the stages no longer need).
+  const float l = half_sum(st.l);
+  if (half == 0) {
+    stat[wave][0][mine] = st.m;
+    stat[wave][1][mine] = l;
+  }
+  __syncthreads();
+  float m = kNoMax, sum = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kSplitWaves; ++w) m = fmaxf(m, stat[w][0][mine]);
+#pragma unroll
+  for (int w = 0; w < kSplitWaves; ++w) sum += stat[w][1][mine] * __builtin_amdgcn_exp2f(stat[w][0][mine] - m);
+  const float f = __builtin_amdgcn_exp2f(st.m - m);
+  // Each wave's own stages hold its scaled accumulators, [d][row]: 32 floats a row of
+  // d, one bank row for the 32 queries.
+  float *acc = reinterpret_cast<float *>(lds[wave]);
+#pragma unroll
+  for (int d = 0; d < kHd / 32; ++d)
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      acc[(32 * d + 8 * (j / 4) + 4 * half + j % 4) * kSplitRows + mine] = st.o[d][j] * f;
+  __syncthreads();
+  // Wave w takes columns w * kHd/4 .. of every row: lane = row (both halves split them).
+  constexpr int kCols = kHd / kSplitWaves / 2;
+  const int d0 = (wave * 2 + half) * kCols;
+  float out[kCols];
+#pragma unroll
+  for (int j = 0; j < kCols; ++j) {
+    float x = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kSplitWaves; ++w)
+      x += reinterpret_cast<const float *>(lds[w])[(d0 + j) * kSplitRows + mine];
+    out[j] = x;
+  }
+  if (mine >= rows) return;
+  if (splits == 1) {
+    const float g = sum > 0.0f ? 1.0f / sum : 0.0f;
+    uint16_t *orow = a.o + (int64_t)qrow * a.os + (int64_t)h * kHd + d0;
+#pragma unroll
+    for (int j = 0; j < kCols; j += 8) {
+      u32x4 w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = pack_bf16(out[j + 2 * e] * g, out[j + 2 * e + 1] * g);
+      *reinterpret_cast<u32x4 *>(orow + j) = w;
+    }
+    if (a.lse && wave == 0 && half == 0)
+      a.lse[(int64_t)h * a.q_tokens + qrow] = sum > 0.0f ? (m + __builtin_log2f(sum)) * kLn2 : -__builtin_inff();
+  } else {
+    float *part = a.ws + ((size_t)((size_t)tile * a.k_heads + hk) * splits + split) * split_floats<kHd>();
+#pragma unroll
+    for (int j = 0; j < kCols; j += 4)
+      *reinterpret_cast<f32x4 *>(part + mine * kHd + d0 + j) = (f32x4){out[j], out[j + 1], out[j + 2], out[j + 3]};
+    if (wave == 0 && half == 0) {
+      part[kSplitRows * kHd + mine] = m;
+      part[kSplitRows * kHd + kSplitRows + mine] = sum;
+    }
+  }
+}
+
+// One wave a row: its lanes take kHd / 64 columns each.
+template <int kHd>
+__global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int splits) {
+  constexpr int kPer = kHd / 64;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int hk = (int)(blockIdx.x % a.k_heads);
+  const int rest = (int)(blockIdx.x / a.k_heads);
+  const int mine = (rest % (kSplitRows / 4)) * 4 + wave, tile = rest / (kSplitRows / 4);
+  int slot = tile;
+  const Seq sq = load_seq(a, find_seq(a.q_start, a.sequences, a.q_tokens, a.group, kSplitRows, slot));
+  if ((int64_t)slot * kSplitRows + mine >= sq.ql * a.group) return;
+  const int r = slot * kSplitRows + mine;
+  const int qrow = sq.q0 + r / a.group, h = hk * a.group + r % a.group;
+  const float *part = a.ws + (size_t)((size_t)tile * a.k_heads + hk) * splits * split_floats<kHd>();
+  float m = kNoMax;
+  for (int s = 0; s < splits; ++s) m = fmaxf(m, part[s * split_floats<kHd>() + kSplitRows * kHd + mine]);
+  float sum = 0.0f, x[kPer] = {};
+  for (int s = 0; s < splits; ++s) {
+    const float *one = part + s * split_floats<kHd>();
+    const float f = __builtin_amdgcn_exp2f(one[kSplitRows * kHd + mine] - m);
+    sum += one[kSplitRows * kHd + kSplitRows + mine] * f;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) x[j] += one[mine * kHd + kPer * lane + j] * f;
+  }
+  const float g = sum > 0.0f ? 1.0f / sum : 0.0f;
+  uint16_t *orow = a.o + (int64_t)qrow * a.os + (int64_t)h * kHd;
+  if (kPer == 2)
+    *reinterpret_cast<uint32_t *>(orow + 2 * lane) = pack_bf16(x[0] * g, x[kPer - 1] * g);
+  else
+    orow[lane] = (uint16_t)pack_bf16(x[0] * g, 0.0f);
+  if (a.lse && lane == 0)
+    a.lse[(int64_t)h * a.q_tokens + qrow] = sum > 0.0f ? (m + __builtin_log2f(sum)) * kLn2 : -__builtin_inff();
+}
+
+template <int kHd>
+hipError_t launch(const AttnArgs &a, const AttnPlan &plan, hipStream_t stream) {
+  if (!plan.split) {
+    attn_kernel<kHd><<<dim3((unsigned)((int64_t)plan.slots * a.q_heads)), dim3(64 * kFwdWaves), 0, stream>>>(a, plan.slots);
+    return hipGetLastError();
+  }
+  attn_split_kernel<kHd><<<dim3((unsigned)((int64_t)plan.slots * a.k_heads * plan.splits)), dim3(64 * kSplitWaves), 0,
+                           stream>>>(a, plan.splits);
+  if (hipError_t e = hipGetLastError()) return e;
+  if (plan.splits > 1) {
+    attn_join_kernel<kHd><<<dim3((unsigned)((int64_t)plan.slots * a.k_heads * (kSplitRows / 4))), dim3(256), 0, stream>>>(
+        a, plan.splits);
+    return hipGetLastError();
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+AttnPlan plan_attention(const puro_attention_shape &a) {
+  AttnPlan p{};
+  p.splits = 1;
+  const int64_t group = a.q_heads / a.k_heads;
+  const int64_t big = a.q_tokens / kFwdRows + a.sequences;
+  const int64_t few = a.q_tokens * group / kSplitRows + a.sequences;
+  p.split = big * a.q_heads < 256;
+  p.slots = (int)(p.split ? few : big);
+  if (p.split) {
+    // Enough workgroups for the 256 compute units twice over, but at least 8 chunks of
+    // keys for each.
+    int64_t keys = a.max_k > 0 ? a.max_k : a.k_tokens / a.sequences;
+    if (a.window > 0 && keys > a.window + a.sinks + 64) keys = a.window + a.sinks + 64;
+    int64_t splits = (512 + few * a.k_heads - 1) / (few * a.k_heads);
+    const int64_t most = keys / (8 * kSplitKeys);
+    if (splits > most) splits = most;
+    if (splits > 128) splits = 128;
+    if (splits < 1) splits = 1;
+    p.splits = (int)splits;
+    if (splits > 1)
+      p.ws_bytes = (size_t)few * (size_t)a.k_heads * (size_t)splits * (size_t)kSplitRows * (size_t)(a.head_dim + 2) * 4;
+  }
+  return p;
+}
+
+hipError_t run_attention(const AttnArgs &a, int head_dim, const AttnPlan &plan, hipStream_t stream) {
+  return head_dim == 128 ? launch<128>(a, plan, stream) : launch<64>(a, plan, stream);
+}
+
+}  // namespace puro

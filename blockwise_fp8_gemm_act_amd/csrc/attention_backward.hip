@@ -1,0 +1,417 @@
+// Attention backward (gfx950).  With P = exp(S - lse), D = rowsum(do o), dS = P
+// (do v^T - D):
+//   dq = scale dS k,   dk = scale dS^T q,   dv = P^T do
+// in two kernels that recompute S: one owns queries and walks the keys (dq, and D
+// on the way), one owns keys and walks the queries of their group (dk, dv).  The
+// scores are computed twice (7 products instead of 5), but every sum has one owner
+// and a fixed order: no atomics, and no fp32 copy of dq in memory.
+#include "attention_common.h"
+
+namespace puro {
+namespace {
+
+__device__ __forceinline__ void wait_all_and_meet() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// ---------------------------------------------------------------- dq
+constexpr int kDqWaves = 4, kDqRows = 32 * kDqWaves, kDqKeys = 64;
+
+// Also writes, for the kernel below, stats[0][h][row] = lse / ln 2 (+infinity for a
+// row that sees nothing: its P are then 0) and stats[1][h][row] = D.
+template <int kHd>
+__global__ void __launch_bounds__(64 * kDqWaves, 2) attn_dq_kernel(AttnArgs a, int slots) {
+  constexpr int kTile = kDqKeys * kHd;
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[2][2][kTile];
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int hk = (int)(blockIdx.x % a.k_heads);
+  const int rest = (int)(blockIdx.x / a.k_heads);
+  const int h = hk * a.group + rest % a.group;
+  int slot = slots - 1 - rest / a.group;
+  const Seq sq = load_seq(a, find_seq(a.q_start, a.sequences, a.q_tokens, 1, kDqRows, slot));
+  if ((int64_t)slot * kDqRows >= sq.ql) return;
+  const int row0 = slot * kDqRows;
+  const int rows = sq.ql - row0 < kDqRows ? sq.ql - row0 : kDqRows;
+  const int shift = sq.kl - sq.ql;
+  const KeyTiles kt = key_tiles(shift + row0, shift + row0 + rows - 1, a.window, a.sinks, kDqKeys);
+
+  const int mine = 32 * wave + (lane & 31);
+  const int qrow = sq.q0 + row0 + (mine < rows ? mine : rows - 1);
+  const int p = shift + row0 + mine;
+  const int w_lo = shift + row0 + 32 * wave, w_hi = w_lo + 31;
+  bf16x8 qf[kHd / 16], df[kHd / 16];
+  float dd = 0.0f;
+#pragma unroll
+  for (int kk = 0; kk < kHd / 16; ++kk) {
+    const int64_t at = (int64_t)h * kHd + 16 * kk + 8 * half;
+    qf[kk] = load8(a.q + (int64_t)qrow * a.qs + at);
+    df[kk] = load8(a.d_o + (int64_t)qrow * a.os + at);
+    const bf16x8 of = load8(a.o + (int64_t)qrow * a.os + at);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dd = __builtin_fmaf((float)df[kk][j], (float)of[j], dd);
+  }
+  dd = half_sum(dd);
+  float lse2 = a.lse[(int64_t)h * a.q_tokens + qrow] * kLog2e;
+  if (lse2 == -__builtin_inff()) lse2 = __builtin_inff();
+  if (half == 0 && mine < rows) {
+    a.ws[(int64_t)h * a.q_tokens + qrow] = lse2;
+    a.ws[(int64_t)(a.q_heads + h) * a.q_tokens + qrow] = dd;
+  }
+
+  const uint16_t *kbase = a.k + (int64_t)sq.k0 * a.ks + (int64_t)hk * kHd;
+  const uint16_t *vbase = a.v + (int64_t)sq.k0 * a.vs + (int64_t)hk * kHd;
+  const uint32_t lds0 = lds_addr(lds);
+  auto copy = [&](int i, int buf) {
+    const int key0 = kt.key0(i, kDqKeys);
+    const uint32_t at = lds0 + (uint32_t)(buf * 2 * kTile * 2);
+#pragma unroll
+    for (int c = wave; c < kDqKeys / kDmaRows<kHd>; c += kDqWaves) {
+      copy_rows<kHd>(at, c * kDmaRows<kHd>, [&](int r) { return kbase + (int64_t)kt.row(key0 + r) * a.ks; });
+      copy_rows<kHd>(at + kTile * 2, c * kDmaRows<kHd>,
+                     [&](int r) { return vbase + (int64_t)kt.row(key0 + r) * a.vs; });
+    }
+  };
+
+  f32x16 acc[kHd / 32];
+#pragma unroll
+  for (int d = 0; d < kHd / 32; ++d) acc[d] = (f32x16){};
+  const float c2 = a.scale * kLog2e;
+  if (kt.count > 0) copy(0, 0);
+  for (int i = 0; i < kt.count; ++i) {
+    wait_all_and_meet();
+    if (i + 1 < kt.count) copy(i + 1, (i + 1) & 1);
+    const int key0 = kt.key0(i, kDqKeys);
+    const uint32_t ktile = lds0 + (uint32_t)((i & 1) * 2 * kTile * 2), vtile = ktile + kTile * 2;
+    const bool none = key0 > w_hi || (a.window > 0 && key0 + kDqKeys - 1 <= w_lo - a.window && key0 >= a.sinks);
+    if (none) continue;
+    const bool all = key0 + kDqKeys - 1 <= w_lo &&
+                     (a.window == 0 || key0 > w_hi - a.window || key0 + kDqKeys <= a.sinks);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      f32x16 s = {}, dp = {};
+#pragma unroll
+      for (int kk = 0; kk < kHd / 16; ++kk) s = mfma(row_frag<kHd>(ktile, 32 * b, kk), qf[kk], s);
+#pragma unroll
+      for (int kk = 0; kk < kHd / 16; ++kk) dp = mfma(row_frag<kHd>(vtile, 32 * b, kk), df[kk], dp);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], c2, -lse2));
+        if (!all) e = visible(key0 + 32 * b + 8 * (j / 4) + 4 * half + j % 4, p, a.window, a.sinks) ? e : 0.0f;
+        s[j] = e * (dp[j] - dd);
+      }
+#pragma unroll
+      for (int step = 0; step < 2; ++step) {
+        const bf16x8 sf = pack_step(s, step);
+#pragma unroll
+        for (int d = 0; d < kHd / 32; ++d) acc[d] = mfma(col_frag<kHd>(ktile, 32 * b + 16 * step, d), sf, acc[d]);
+      }
+    }
+  }
+  if (mine < rows) {
+    uint16_t *out = a.dq + (int64_t)qrow * a.dqs + (int64_t)h * kHd;
+#pragma unroll
+    for (int d = 0; d < kHd / 32; ++d) store_block(out + 32 * d, acc[d], a.scale);
+  }
+}
+
+// ---------------------------------------------------------------- dk, dv
+constexpr int kDkWaves = 4, kDkRows = 32 * kDkWaves, kDkQueries = 64;
+
+// Work of one block of 128 keys and one key head: tiles of 64 queries of each head
+// of the group.  `near` tiles are those whose queries have the block in their
+// window; where the block holds first keys, `far` tiles are those past it, which
+// see the first keys only.  Both are cut into parts, so that a long walk (many
+// heads, few keys; first keys under a long sequence) is shared by workgroups, which
+// then leave fp32 partials for the join.
+struct DkPlan {
+  int slots;          // key blocks, empty ones included
+  int parts;          // of the near tiles
+  int far_blocks;     // key blocks of a sequence that hold first keys; 0: no far work
+  int far_parts;
+  size_t near_at, far_at, floats;   // partials in the workspace (floats from its start)
+};
+
+template <int kHd>
+__host__ __device__ constexpr size_t part_floats() {
+  return (size_t)2 * kDkRows * kHd;
+}
+
+__device__ __forceinline__ void dma4(const void *src, uint32_t lds) {
+  uint32_t save;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %2\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dword %1, off\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(save)
+      : "v"(src), "s"(lds)
+      : "memory");
+}
+
+template <int kHd>
+__global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a, DkPlan plan) {
+  constexpr int kTile = kDkQueries * kHd;
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[2][2][kTile];
+  __shared__ __attribute__((aligned(1024))) float stat[2][2][kDkQueries];
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int hk = (int)(blockIdx.x % a.k_heads);
+  int rest = (int)(blockIdx.x / a.k_heads);
+  const int far_items = a.sequences * plan.far_blocks * plan.far_parts;
+  const bool far = rest < far_items;
+  int part, parts, slot, s;
+  float *partial = nullptr;
+  if (far) {
+    part = rest % plan.far_parts;
+    parts = plan.far_parts;
+    s = rest / plan.far_parts / plan.far_blocks;
+    slot = rest / plan.far_parts % plan.far_blocks;
+    partial = a.ws + plan.far_at +
+              ((size_t)((s * plan.far_blocks + slot) * a.k_heads + hk) * (plan.far_parts + 1) + part) * part_floats<kHd>();
+  } else {
+    rest -= far_items;
+    part = rest % plan.parts;
+    parts = plan.parts;
+    slot = rest / plan.parts;
+    const int number = slot;
+    s = find_seq(a.k_start, a.sequences, a.k_tokens, 1, kDkRows, slot);
+    if (parts > 1)
+      partial = a.ws + plan.near_at + ((size_t)(number * a.k_heads + hk) * parts + part) * part_floats<kHd>();
+    else if (slot < plan.far_blocks)
+      partial = a.ws + plan.far_at +
+                ((size_t)((s * plan.far_blocks + slot) * a.k_heads + hk) * (plan.far_parts + 1) + plan.far_parts) *
+                    part_floats<kHd>();
+  }
+  const Seq sq = load_seq(a, s);
+  if ((int64_t)slot * kDkRows >= sq.kl) return;
+  const int key0 = slot * kDkRows;
+  const int keys = sq.kl - key0 < kDkRows ? sq.kl - key0 : kDkRows;
+  const int shift = sq.kl - sq.ql;
+
+  // Queries (as numbers in the sequence) that this work sees.
+  int q_lo = key0 - shift, q_hi = sq.ql - 1;
+  // The last query with the block in its window; without far work first keys are seen to the end.
+  const bool windowed = a.window > 0 && (key0 >= a.sinks || slot < plan.far_blocks);
+  const int q_near = windowed ? key0 + keys - 1 + a.window - 1 - shift : q_hi;
+  if (far) q_lo = q_near + 1 > q_lo ? q_near + 1 : q_lo;
+  else if (q_near < q_hi) q_hi = q_near;
+  if (q_lo < 0) q_lo = 0;
+  const int tile0 = q_lo / kDkQueries;
+  const int tiles = q_lo <= q_hi ? q_hi / kDkQueries - tile0 + 1 : 0;
+  const int64_t work = (int64_t)tiles * a.group;
+  const int begin = (int)(work * part / parts), end = (int)(work * (part + 1) / parts);
+
+  const int mine = 32 * wave + (lane & 31);
+  const int krow = sq.k0 + key0 + (mine < keys ? mine : keys - 1);
+  const int key = key0 + mine;
+  const int w_lo = key0 + 32 * wave, w_hi = w_lo + 31;
+  bf16x8 kf[kHd / 16], vf[kHd / 16];
+#pragma unroll
+  for (int kk = 0; kk < kHd / 16; ++kk) {
+    const int64_t at = (int64_t)hk * kHd + 16 * kk + 8 * half;
+    kf[kk] = load8(a.k + (int64_t)krow * a.ks + at);
+    vf[kk] = load8(a.v + (int64_t)krow * a.vs + at);
+  }
+
+  const uint32_t lds0 = lds_addr(lds), stat0 = lds_addr(stat);
+  auto copy = [&](int i, int buf) {
+    const int h = hk * a.group + i / tiles;
+    const int q0 = (tile0 + i % tiles) * kDkQueries;
+    const uint32_t at = lds0 + (uint32_t)(buf * 2 * kTile * 2);
+    auto row = [&](int r) { return (int64_t)(sq.q0 + (q0 + r < sq.ql ? q0 + r : sq.ql - 1)); };
+    const uint16_t *qb = a.q + (int64_t)h * kHd, *db = a.d_o + (int64_t)h * kHd;
+#pragma unroll
+    for (int c = wave; c < kDkQueries / kDmaRows<kHd>; c += kDkWaves) {
+      copy_rows<kHd>(at, c * kDmaRows<kHd>, [&](int r) { return qb + row(r) * a.qs; });
+      copy_rows<kHd>(at + kTile * 2, c * kDmaRows<kHd>, [&](int r) { return db + row(r) * a.os; });
+    }
+    if (wave < 2)
+      dma4(a.ws + (int64_t)(wave * a.q_heads + h) * a.q_tokens + row(lane),
+           __builtin_amdgcn_readfirstlane(stat0 + (uint32_t)((buf * 2 + wave) * kDkQueries * 4)));
+  };
+
+  f32x16 dk[kHd / 32], dv[kHd / 32];
+#pragma unroll
+  for (int d = 0; d < kHd / 32; ++d) dk[d] = dv[d] = (f32x16){};
+  const float c2 = a.scale * kLog2e;
+  if (begin < end) copy(begin, 0);
+  for (int i = begin; i < end; ++i) {
+    const int buf = (i - begin) & 1;
+    wait_all_and_meet();
+    if (i + 1 < end) copy(i + 1, buf ^ 1);
+    const int q0 = (tile0 + i % tiles) * kDkQueries;
+    const uint32_t qtile = lds0 + (uint32_t)(buf * 2 * kTile * 2), dtile = qtile + kTile * 2;
+#pragma unroll 1
+    for (int b = 0; b < 2; ++b) {
+      const int p_lo = shift + q0 + 32 * b, p_hi = p_lo + 31;
+      // Far work starts inside a tile: queries before it belong to the near work.
+      const int first = far ? shift + q_lo : 0;
+      const bool none = q0 + 32 * b >= sq.ql || w_lo > p_hi || p_hi < first ||
+                        (a.window > 0 && w_hi <= p_lo - a.window && w_lo >= a.sinks);
+      if (none) continue;
+      const bool all = q0 + 32 * b + 31 < sq.ql && w_hi <= p_lo && p_lo >= first && (far || p_hi <= shift + q_hi) &&
+                       (a.window == 0 || w_lo > p_hi - a.window || w_hi < a.sinks);
+      f32x16 s = {}, dp = {};
+#pragma unroll
+      for (int kk = 0; kk < kHd / 16; ++kk) s = mfma(row_frag<kHd>(qtile, 32 * b, kk), kf[kk], s);
+#pragma unroll
+      for (int kk = 0; kk < kHd / 16; ++kk) dp = mfma(row_frag<kHd>(dtile, 32 * b, kk), vf[kk], dp);
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 lse2 = *reinterpret_cast<const f32x4 *>(&stat[buf][0][32 * b + 8 * g + 4 * half]);
+        const f32x4 dd = *reinterpret_cast<const f32x4 *>(&stat[buf][1][32 * b + 8 * g + 4 * half]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = 4 * g + e;
+          float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], c2, -lse2[e]));
+          if (!all) {
+            const int qi = q0 + 32 * b + 8 * g + 4 * half + e;
+            x = qi <= q_hi && shift + qi >= first && visible(key, shift + qi, a.window, a.sinks) ? x : 0.0f;
+          }
+          s[j] = x;
+          dp[j] = x * (dp[j] - dd[e]);
+        }
+      }
+#pragma unroll
+      for (int step = 0; step < 2; ++step) {
+        const bf16x8 pf = pack_step(s, step), sf = pack_step(dp, step);
+#pragma unroll
+        for (int d = 0; d < kHd / 32; ++d) {
+          dv[d] = mfma(col_frag<kHd>(dtile, 32 * b + 16 * step, d), pf, dv[d]);
+          dk[d] = mfma(col_frag<kHd>(qtile, 32 * b + 16 * step, d), sf, dk[d]);
+        }
+      }
+    }
+  }
+
+  if (partial) {
+    // [dk, dv][key][column]: registers 4g .. 4g+3 are 4 consecutive columns.
+    float *pk = partial + mine * kHd, *pv = pk + kDkRows * kHd;
+#pragma unroll
+    for (int d = 0; d < kHd / 32; ++d)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int c = 32 * d + 8 * g + 4 * half;
+        *reinterpret_cast<f32x4 *>(pk + c) = (f32x4){dk[d][4 * g], dk[d][4 * g + 1], dk[d][4 * g + 2], dk[d][4 * g + 3]};
+        *reinterpret_cast<f32x4 *>(pv + c) = (f32x4){dv[d][4 * g], dv[d][4 * g + 1], dv[d][4 * g + 2], dv[d][4 * g + 3]};
+      }
+  } else if (mine < keys) {
+    uint16_t *ok = a.dk + (int64_t)krow * a.dks + (int64_t)hk * kHd;
+    uint16_t *ov = a.dv + (int64_t)krow * a.dvs + (int64_t)hk * kHd;
+#pragma unroll
+    for (int d = 0; d < kHd / 32; ++d) {
+      store_block(ok + 32 * d, dk[d], a.scale);
+      store_block(ov + 32 * d, dv[d], 1.0f);
+    }
+  }
+}
+
+// Sums the partials of a key block in order: 8 columns a thread.
+template <int kHd>
+__global__ void __launch_bounds__(256) attn_dkdv_join_kernel(AttnArgs a, DkPlan plan) {
+  constexpr int kThreads = kHd / 8, kRows = 256 / kThreads, kChunks = kDkRows / kRows;
+  const int hk = (int)(blockIdx.x % a.k_heads);
+  const int rest = (int)(blockIdx.x / a.k_heads);
+  const int number = rest / kChunks;
+  int slot = number;
+  const int s = find_seq(a.k_start, a.sequences, a.k_tokens, 1, kDkRows, slot);
+  const Seq sq = load_seq(a, s);
+  const bool far = slot < plan.far_blocks;
+  if (plan.parts == 1 && !far) return;
+  const int r = (rest % kChunks) * kRows + (int)threadIdx.x / kThreads, c = 8 * ((int)threadIdx.x % kThreads);
+  if ((int64_t)slot * kDkRows + r >= sq.kl) return;
+  float x[2][8] = {};
+  auto add = [&](const float *from) {
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int j = 0; j < 8; j += 4) {
+        const f32x4 v = *reinterpret_cast<const f32x4 *>(from + (w * kDkRows + r) * kHd + c + j);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[w][j + e] += v[e];
+      }
+  };
+  if (plan.parts > 1)
+    for (int p = 0; p < plan.parts; ++p)
+      add(a.ws + plan.near_at + ((size_t)(number * a.k_heads + hk) * plan.parts + p) * part_floats<kHd>());
+  if (far) {
+    const float *from = a.ws + plan.far_at +
+                        (size_t)((s * plan.far_blocks + slot) * a.k_heads + hk) * (plan.far_parts + 1) * part_floats<kHd>();
+    for (int p = 0; p < plan.far_parts + (plan.parts == 1); ++p) add(from + p * part_floats<kHd>());
+  }
+  const int64_t row = sq.k0 + slot * kDkRows + r;
+  u32x4 k, v;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    k[j] = pack_bf16(x[0][2 * j] * a.scale, x[0][2 * j + 1] * a.scale);
+    v[j] = pack_bf16(x[1][2 * j], x[1][2 * j + 1]);
+  }
+  *reinterpret_cast<u32x4 *>(a.dk + row * a.dks + (int64_t)hk * kHd + c) = k;
+  *reinterpret_cast<u32x4 *>(a.dv + row * a.dvs + (int64_t)hk * kHd + c) = v;
+}
+
+// The plan from sizes alone (host).
+DkPlan plan_dk(int64_t q_tokens, int64_t k_tokens, int64_t sequences, int64_t q_heads, int64_t k_heads, int64_t head_dim,
+               int64_t window, int64_t sinks) {
+  DkPlan p{};
+  const int64_t floats = 2 * kDkRows * head_dim;
+  p.slots = (int)(k_tokens / kDkRows + sequences);
+  const int64_t group = q_heads / k_heads;
+  const int64_t per_seq = (q_tokens + sequences - 1) / sequences;
+  // Near tiles of a block, and parts of at least 8 of them where the blocks alone do
+  // not fill the card twice over.
+  int64_t seen = window > 0 && window + kDkRows < per_seq ? window + kDkRows : per_seq;
+  int64_t parts = 512 / ((int64_t)p.slots * k_heads);
+  const int64_t most = seen / kDkQueries * group / 8;
+  if (parts > most) parts = most;
+  if (parts > 16) parts = 16;
+  p.parts = (int)(parts < 1 ? 1 : parts);
+  p.near_at = (size_t)2 * q_heads * q_tokens;
+  p.near_at = (p.near_at + 63) / 64 * 64;
+  p.floats = p.near_at + (p.parts > 1 ? (size_t)p.slots * k_heads * p.parts * floats : 0);
+  p.far_at = p.floats;
+  // Far work pays where a sequence is several windows long; many first keys make
+  // enough blocks by themselves, and partials for them would be large.
+  int64_t far = per_seq / (window + kDkRows);
+  if (far > 32) far = 32;
+  if (window > 0 && sinks > 0 && sinks <= 2 * kDkRows && far >= 2) {
+    p.far_blocks = (int)((sinks + kDkRows - 1) / kDkRows);
+    p.far_parts = (int)far;
+    p.floats += (size_t)sequences * p.far_blocks * k_heads * (p.far_parts + 1) * floats;
+  }
+  return p;
+}
+
+template <int kHd>
+hipError_t launch(const AttnArgs &a, hipStream_t stream) {
+  if (a.q_tokens > 0) {
+    const int slots = a.q_tokens / kDqRows + a.sequences;
+    attn_dq_kernel<kHd><<<dim3((unsigned)((int64_t)slots * a.q_heads)), dim3(64 * kDqWaves), 0, stream>>>(a, slots);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  if (a.k_tokens == 0) return hipSuccess;
+  const DkPlan plan = plan_dk(a.q_tokens, a.k_tokens, a.sequences, a.q_heads, a.k_heads, kHd, a.window, a.sinks);
+  const int64_t items = (int64_t)a.sequences * plan.far_blocks * plan.far_parts + (int64_t)plan.slots * plan.parts;
+  attn_dkdv_kernel<kHd><<<dim3((unsigned)(items * a.k_heads)), dim3(64 * kDkWaves), 0, stream>>>(a, plan);
+  if (hipError_t e = hipGetLastError()) return e;
+  if (plan.parts > 1 || plan.far_blocks > 0) {
+    const int chunks = kDkRows / (256 / (kHd / 8));
+    attn_dkdv_join_kernel<kHd><<<dim3((unsigned)((int64_t)plan.slots * chunks * a.k_heads)), dim3(256), 0, stream>>>(a, plan);
+    return hipGetLastError();
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+size_t attention_backward_ws_bytes(const puro_attention_shape &a) {
+  return plan_dk(a.q_tokens, a.k_tokens, a.sequences, a.q_heads, a.k_heads, a.head_dim, a.window, a.sinks).floats * 4;
+}
+
+hipError_t run_attention_backward(const AttnArgs &a, int head_dim, hipStream_t stream) {
+  return head_dim == 128 ? launch<128>(a, stream) : launch<64>(a, stream);
+}
+
+}  // namespace puro

@@ -1,0 +1,223 @@
+// Device pieces shared by the attention kernels (gfx950): sequence lookup, the
+// mask, LDS tiles and their two reads, the bf16 matrix product.
+//
+// Every kernel works on transposed score tiles: a 32x32x16 MFMA with 32 keys as
+// rows and 32 queries as columns leaves lane l with query l & 31 and 16 of the 32
+// keys, register i holding key 8 (i/4) + 4 (l/32) + i%4.  A softmax row is then
+// one lane and its partner 32 lanes away, statistics are scalars of the lane, and
+// the probabilities are, in place, the B operand of the next product: registers
+// 8s .. 8s+7 are the 8 keys a lane feeds to contraction step s, in the order {0-3,
+// 8-11} for lanes below 32 and {4-7, 12-15} above, which the A operand's read
+// follows.
+#pragma once
+
+#include "device_common.h"
+#include "launch_attention.h"
+
+namespace puro {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// Running maximum of a row that has seen nothing: finite, so that differences of
+// maxima never are inf - inf; every score of the contract is far above it.
+constexpr float kNoMax = -1e30f;
+
+__device__ __forceinline__ f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ bf16x8 load8(const uint16_t *p) { return *reinterpret_cast<const bf16x8 *>(p); }
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
+}
+
+// The other half wave's value: lanes 0-31 and 32-63 exchange.
+__device__ __forceinline__ float half_max(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// ---------------------------------------------------------------- sequences
+struct Seq {
+  int q0, ql, k0, kl;    // first rows and lengths
+};
+
+__device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
+
+// Starts and lengths come from device memory: clamped, so that no row outside the
+// tensors is ever addressed.
+__device__ __forceinline__ Seq load_seq(const AttnArgs &a, int s) {
+  Seq r;
+  if (!a.q_start) return Seq{0, a.q_tokens, 0, a.k_len ? clampi(a.k_len[0], 0, a.k_tokens) : a.k_tokens};
+  r.q0 = clampi(a.q_start[s], 0, a.q_tokens);
+  r.ql = clampi(a.q_start[s + 1], r.q0, a.q_tokens) - r.q0;
+  r.k0 = clampi(a.k_start[s], 0, a.k_tokens);
+  r.kl = clampi(a.k_start[s + 1], r.k0, a.k_tokens) - r.k0;
+  if (a.k_len) r.kl = clampi(a.k_len[s], 0, r.kl);
+  return r;
+}
+
+// Tiles of `unit` rows are numbered over all sequences without a prefix sum:
+// sequence s owns the numbers from start(s) * mul / unit + s up to that of s + 1.
+// These are never fewer than its tiles; the surplus ones are empty.  Returns the
+// sequence of tile `slot` and subtracts its first number.
+__device__ __forceinline__ int find_seq(const int32_t *start, int sequences, int tokens, int mul, int unit, int &slot) {
+  if (!start) return 0;
+  const int lane = threadIdx.x & 63;
+  int s = 0, first = 0;
+  for (int b = 0; b < sequences; b += 64) {
+    const int i = b + lane;
+    const int base = i < sequences ? (int)((int64_t)clampi(start[i], 0, tokens) * mul / unit) + i : 0x7fffffff;
+    const uint64_t le = __ballot(base <= slot);
+    if (!le) break;
+    const int n = 63 - __builtin_clzll(le);
+    s = b + n;
+    first = __builtin_amdgcn_readlane(base, n);
+  }
+  slot -= first;
+  return s;
+}
+
+// ---------------------------------------------------------------- mask
+__device__ __forceinline__ bool visible(int key, int p, int window, int sinks) {
+  return key <= p && (window == 0 || key > p - window || key < sinks);
+}
+
+// The key tiles that a block of queries at positions p_lo .. p_hi looks at, `unit`
+// keys each: those of the visible first keys, then those of the window.  Keys that
+// none of these queries sees are read from row `lo` or `hi` instead (they are
+// masked), so that what such rows hold never matters.
+struct KeyTiles {
+  int first_n, main0, count;    // tiles of the first keys; first tile of the window; all
+  int lo, hi, sinks;
+  __device__ __forceinline__ int key0(int i, int unit) const { return (i < first_n ? i : main0 + i - first_n) * unit; }
+  __device__ __forceinline__ int row(int key) const { return key < sinks ? key : clampi(key, lo, hi); }
+};
+
+__device__ __forceinline__ KeyTiles key_tiles(int p_lo, int p_hi, int window, int sinks, int unit) {
+  KeyTiles t;
+  t.hi = p_hi;
+  t.lo = window > 0 && p_lo >= window ? p_lo - window + 1 : 0;
+  t.sinks = sinks < t.lo ? sinks : t.lo;
+  t.main0 = t.lo / unit;
+  t.first_n = (t.sinks + unit - 1) / unit;
+  if (t.first_n > t.main0) t.first_n = t.main0;
+  t.count = p_hi < 0 ? 0 : t.first_n + p_hi / unit - t.main0 + 1;
+  return t;
+}
+
+// ---------------------------------------------------------------- LDS tiles
+// A tile holds rows of kHd bf16; the 16-byte chunk c of row r sits at c ^ swz(r).
+// Row fragments (32 rows, one chunk) are read 16 lanes at a time, transposed
+// fragments as 4 rows by 64 bytes; over the 64 banks with their bit-8 hash both
+// touch every bank once under these swizzles.
+template <int kHd>
+__device__ __forceinline__ int swz(int r) {
+  if (kHd == 128) return ((r & 3) << 2) | ((r >> 2) & 3);
+  return ((r & 2) << 1) | ((r >> 1) & 2) | ((r >> 3) & 1);
+}
+
+// Global -> LDS copy of 16 bytes a lane to lds + 16 lane.  Asm, so that the
+// compiler does not make every later LDS read wait for it: completion is awaited
+// explicitly.
+__device__ __forceinline__ void dma16(const void *src, uint32_t lds) {
+  uint32_t save;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %2\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, off\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(save)
+      : "v"(src), "s"(lds)
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t lds_addr(const void *p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
+}
+
+// One 1 KB copy: kRows rows of a tile starting at row r0 (a multiple of kRows);
+// src_row(r) gives the global row that tile row r holds, as a pointer.
+template <int kHd>
+constexpr int kDmaRows = 512 / kHd;    // rows of one copy: 4 or 8
+
+template <int kHd, typename F>
+__device__ __forceinline__ void copy_rows(uint32_t tile, int r0, F src_row) {
+  const int lane = threadIdx.x & 63;
+  const int r = r0 + lane / (kHd / 8), c = lane % (kHd / 8);
+  const uint16_t *p = src_row(r) + 8 * (c ^ swz<kHd>(r));
+  dma16(p, __builtin_amdgcn_readfirstlane(tile + (uint32_t)r0 * kHd * 2));
+}
+
+typedef __attribute__((address_space(3))) bf16x8 lds_bf16x8;
+typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
+
+// Rows r0 .. r0+31, contraction step kk (16 columns): lane l gets row r0 + (l & 31),
+// columns 16 kk + 8 (l / 32) .. +7.
+template <int kHd>
+__device__ __forceinline__ bf16x8 row_frag(uint32_t tile, int r0, int kk) {
+  const int lane = threadIdx.x & 63;
+  const int r = lane & 31;
+  const uint32_t at = tile + (uint32_t)(r * kHd * 2) + (uint32_t)(((2 * kk + (lane >> 5)) ^ swz<kHd>(r)) * 16);
+  return *(lds_bf16x8 *)(uintptr_t)(at + (uint32_t)(r0 * kHd * 2));
+}
+
+// The transpose's fragment: lane l gets column 32 db + (l & 31) of the 8 rows r0 +
+// 4 (l / 32) + {0-3, 8-11}; r0 a multiple of 16.  Each 16 lanes read 4 rows by 16
+// columns, 8 bytes a lane, and get them transposed.
+template <int kHd>
+__device__ __forceinline__ bf16x8 col_frag(uint32_t tile, int r0, int db) {
+  const int lane = threadIdx.x & 63;
+  const int half = lane >> 5, i = lane & 15;
+  const int col = 32 * db + (lane & 16) + 4 * (i & 3);
+  bf16x4 v[2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const int r = 4 * half + 8 * w + (i >> 2);
+    const uint32_t at = tile + (uint32_t)(r * kHd * 2) + (uint32_t)(((col >> 3) ^ swz<kHd>(r)) * 16 + (col & 7) * 2);
+    v[w] = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4 *)(uintptr_t)(at + (uint32_t)(r0 * kHd * 2)));
+  }
+  return __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Registers 8s .. 8s+7 of a score tile as the B operand of step s.
+__device__ __forceinline__ bf16x8 pack_step(const f32x16 &p, int s) {
+  u32x4 w;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = pack_bf16(p[8 * s + 2 * j], p[8 * s + 2 * j + 1]);
+  return __builtin_bit_cast(bf16x8, w);
+}
+
+// One block of 32 columns of a transposed accumulator (column of the result = lane
+// & 31's row, register i = column 8 (i/4) + 4 (lane/32) + i%4) to a bf16 row: the
+// half waves exchange so that each lane stores 16 bytes twice.
+__device__ __forceinline__ void store_block(uint16_t *row, const f32x16 &x, float f) {
+  const int half = (threadIdx.x & 63) >> 5;
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    u32x4 w;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const auto r = __builtin_amdgcn_permlane32_swap(pack_bf16(x[8 * g + 2 * j] * f, x[8 * g + 2 * j + 1] * f),
+                                                      pack_bf16(x[8 * g + 4 + 2 * j] * f, x[8 * g + 5 + 2 * j] * f),
+                                                      false, false);
+      w[j] = r[0];
+      w[2 + j] = r[1];
+    }
+    *reinterpret_cast<u32x4 *>(row + 16 * g + 8 * half) = w;
+  }
+}
+
+}  // namespace puro

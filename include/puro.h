@@ -72,8 +72,9 @@ typedef enum {
     PURO_ERR_DEVICE = 7,      /* the current device is not gfx950, or no device */
     PURO_ERR_LAUNCH = 8,      /* the HIP runtime reported an error while enqueueing */
     PURO_ERR_ALIAS = 9,       /* an output overlaps an input or another output */
-    PURO_ERR_SCRATCH = 10     /* puro_gemm_fp8_blockwise_noalloc: the shape needs more split-K
+    PURO_ERR_SCRATCH = 10,    /* puro_gemm_fp8_blockwise_noalloc: the shape needs more split-K
                                  scratch than the library holds (PURO_SCRATCH_BYTES) */
+    PURO_ERR_VALUE = 11       /* a scalar argument is out of its range (puro_attention.h) */
 } puro_status;
 
 typedef enum {
