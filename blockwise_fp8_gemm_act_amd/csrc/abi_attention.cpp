@@ -17,6 +17,7 @@ namespace {
 
 constexpr int64_t kMaxPositions = int64_t(1) << 24;
 constexpr int64_t kMaxRows = int64_t(1) << 30;      // of q and of k: positions plus a window stay in 32 bits
+constexpr int64_t kMaxStride = int64_t(1) << 23;    // 64 rows of it stay in 32 bits of bytes
 
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -53,7 +54,7 @@ bool any_alias(const Rows *in, int nin, const Rows *out, int nout) {
 }
 
 bool strided_ok(int64_t rows, int64_t width, int64_t stride) {
-  return stride >= width && stride % 8 == 0 && shape_ok(rows, width) && shape_ok(rows, stride);
+  return stride >= width && stride < kMaxStride && stride % 8 == 0 && shape_ok(rows, width) && shape_ok(rows, stride);
 }
 
 bool head_dim_ok(int64_t d) { return d == 64 || d == 128; }

@@ -19,13 +19,21 @@ __device__ __forceinline__ f32x16 score_tile(uint32_t ktile, int r0, const bf16x
   return s;
 }
 
+// Masks the scores of keys key0 .. key0+31 for the lane's query at p.
 __device__ __forceinline__ void mask_tile(f32x16 &s, int key0, int p, int window, int sinks) {
   const int half = (threadIdx.x & 63) >> 5;
+  if (key0 < sinks) {                   // first keys that stay visible among them
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int key = key0 + 8 * (i / 4) + 4 * half + i % 4;
-    s[i] = visible(key, p, window, sinks) ? s[i] : -__builtin_inff();
+    for (int i = 0; i < 16; ++i) s[i] = visible(key0 + 8 * (i / 4) + 4 * half + i % 4, p, window, sinks) ? s[i] : -__builtin_inff();
+    return;
   }
+  // p - key is negative for keys after p: causality and the window are one unsigned
+  // comparison.
+  int before = p - key0 - 4 * half;
+  asm volatile("" : "+v"(before));      // keeps the comparisons inside the caller's branch
+  const uint32_t reach = window == 0 ? 0x7fffffffu : (uint32_t)window;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s[i] = (uint32_t)(before - (8 * (i / 4) + i % 4)) < reach ? s[i] : -__builtin_inff();
 }
 
 // Softmax state of one query (of a lane and its partner): m is the maximum in use,
@@ -67,94 +75,191 @@ __device__ __forceinline__ float tile_max(const f32x16 &s) {
 // ---------------------------------------------------------------- many queries
 constexpr int kFwdWaves = 8, kFwdRows = 32 * kFwdWaves, kFwdKeys = 64;
 
+// The two waves of a SIMD take turns: while one multiplies (scores of the next tile,
+// values of this one), the other does the softmax of its next tile, with a barrier
+// between the turns.  Waves 4-7 run one turn behind waves 0-3.
+//
+//   turn          2i                 2i+1               2i+2
+//   waves 0-3     multiply i         softmax i+1        multiply i+1
+//   waves 4-7     softmax i          multiply i         softmax i+1
+//
+// multiply i reads the keys of tile i+1 and the values of tile i, and between its
+// products starts copies of the keys of tile i+3 and the values of tile i+2, each wave
+// its part; they are awaited a turn later, at the end of softmax i+1, and needed two
+// turns after that.  With three places each for keys and values, the places they take
+// were read for the last time two turns before.  (Issued together, a tile's copies
+// stall their wave for 700 to 1000 cycles, as long as the softmax.)
+__device__ __forceinline__ void meet() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
 template <int kHd>
-__global__ void __launch_bounds__(64 * kFwdWaves, 2) attn_kernel(AttnArgs a, int slots) {
-  constexpr int kTile = kFwdKeys * kHd;
-  __shared__ __attribute__((aligned(1024))) uint16_t lds[2][2][kTile];
+__global__ void __launch_bounds__(64 * kFwdWaves, 2) attn_kernel(AttnArgs a, int slots, int fold) {
+  constexpr int kTile = kTileBytes<kHd>(kFwdKeys);
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[6 * kTile];     // three places of keys, three of values
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const bool late = wave >= kFwdWaves / 2;
   // Key heads run fastest over the workgroups, so that with 8 of them each XCD's L2
   // serves one; the last tiles of a sequence, which see most keys, start first.
   const int hk = (int)(blockIdx.x % a.k_heads);
   const int rest = (int)(blockIdx.x / a.k_heads);
   const int h = hk * a.group + rest % a.group;
   int slot = slots - 1 - rest / a.group;
-  const Seq sq = load_seq(a, find_seq(a.q_start, a.sequences, a.q_tokens, 1, kFwdRows, slot));
-  if ((int64_t)slot * kFwdRows >= sq.ql) return;
-  const int row0 = slot * kFwdRows;
-  const int rows = sq.ql - row0 < kFwdRows ? sq.ql - row0 : kFwdRows;
+  const Seq sq = load_seq(a, find_seq(a.q_start, a.sequences, a.q_tokens, 1, kFwdRows * fold, slot));
+  const int tiles = (int)(((int64_t)sq.ql + kFwdRows - 1) / kFwdRows);
+  if ((int64_t)slot * fold >= tiles) return;
   const int shift = sq.kl - sq.ql;                              // position of query 0
-  const KeyTiles kt = key_tiles(shift + row0, shift + row0 + rows - 1, a.window, a.sinks, kFwdKeys);
-
-  const int mine = 32 * wave + (lane & 31);                     // this lane's query in the block
-  const int qrow = sq.q0 + row0 + (mine < rows ? mine : rows - 1);
-  const int p = shift + row0 + mine;
-  const int w_lo = shift + row0 + 32 * wave, w_hi = w_lo + 31;  // positions of the wave's queries
-  bf16x8 qf[kHd / 16];
-#pragma unroll
-  for (int kk = 0; kk < kHd / 16; ++kk)
-    qf[kk] = load8(a.q + (int64_t)qrow * a.qs + (int64_t)h * kHd + 16 * kk + 8 * half);
-
-  const uint16_t *kbase = a.k + (int64_t)sq.k0 * a.ks + (int64_t)hk * kHd;
-  const uint16_t *vbase = a.v + (int64_t)sq.k0 * a.vs + (int64_t)hk * kHd;
+  const TileCopy<kHd> keys(a.k + (int64_t)sq.k0 * a.ks + (int64_t)hk * kHd, a.ks);
+  const TileCopy<kHd> vals(a.v + (int64_t)sq.k0 * a.vs + (int64_t)hk * kHd, a.vs);
   const uint32_t lds0 = lds_addr(lds);
-  auto copy = [&](int i, int buf) {
-    const int key0 = kt.key0(i, kFwdKeys);
-    const uint32_t at = lds0 + (uint32_t)(buf * 2 * kTile * 2);
-#pragma unroll
-    for (int c = wave; c < kFwdKeys / kDmaRows<kHd>; c += kFwdWaves) {
-      copy_rows<kHd>(at, c * kDmaRows<kHd>, [&](int r) { return kbase + (int64_t)kt.row(key0 + r) * a.ks; });
-      copy_rows<kHd>(at + kTile * 2, c * kDmaRows<kHd>,
-                     [&](int r) { return vbase + (int64_t)kt.row(key0 + r) * a.vs; });
-    }
-  };
-
-  Row<kHd> st;
-  st.clear();
   const float c2 = a.scale * kLog2e;
-  if (kt.count > 0) copy(0, 0);
-  for (int i = 0; i < kt.count; ++i) {
-    // This tile has landed, and every wave is done with the other buffer.
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (i + 1 < kt.count) copy(i + 1, (i + 1) & 1);
-    const int key0 = kt.key0(i, kFwdKeys);
-    const uint32_t ktile = lds0 + (uint32_t)((i & 1) * 2 * kTile * 2), vtile = ktile + kTile * 2;
-    const bool none = key0 > w_hi || (a.window > 0 && key0 + kFwdKeys - 1 <= w_lo - a.window && key0 >= a.sinks);
-    if (none) continue;
-    const bool all = key0 + kFwdKeys - 1 <= w_lo &&
-                     (a.window == 0 || key0 > w_hi - a.window || key0 + kFwdKeys <= a.sinks);
+
+  // With fold 2 a workgroup takes a sequence's tile from its end and the one as far
+  // from its start: together they see the same number of keys everywhere.
+  for (int turn = 0; turn < fold; ++turn) {
+    const int tile = turn == 0 && fold == 2 ? tiles - 1 - slot : slot;
+    if (turn == 1 && tile == tiles - 1 - slot) break;
+    const int row0 = tile * kFwdRows;
+    const int rows = sq.ql - row0 < kFwdRows ? sq.ql - row0 : kFwdRows;
+    const KeyTiles kt = key_tiles(shift + row0, shift + row0 + rows - 1, a.window, a.sinks, kFwdKeys);
+    const int mine = 32 * wave + (lane & 31);                     // this lane's query in the block
+    const int qrow = sq.q0 + row0 + (mine < rows ? mine : rows - 1);
+    const int p = shift + row0 + mine;
+    const int w_lo = shift + row0 + 32 * wave, w_hi = w_lo + 31;  // positions of the wave's queries
+    // Tiles past the wave's last query are only copied for the others.
+    int seen = kt.count;
+    while (seen > 0 && kt.key0(seen - 1, kFwdKeys) > w_hi) --seen;
+    bf16x8 qf[kHd / 16];
+#pragma unroll
+    for (int kk = 0; kk < kHd / 16; ++kk)
+      qf[kk] = load8(a.q + (int64_t)qrow * a.qs + (int64_t)h * kHd + 16 * kk + 8 * half);
+
+    // Opaque, so that a read's address stays one register plus a constant.
+    auto place = [&](int n) {
+      uint32_t at = lds0 + (uint32_t)(n * kTile);
+      asm("" : "+s"(at));
+      return at;
+    };
+    auto key_place = [&](int i) { return place(i % 3); };
+    auto value_place = [&](int i) { return place(3 + i % 3); };
+    // This wave's part of a tile's copies, in kParts groups.  Past the last tile that one
+    // is copied again, to a place that is not read any more.
+    constexpr int kParts = kFwdKeys / kGroupRows<kHd> / kFwdWaves;
+    auto copy_keys = [&](int i, int part) {
+      keys(kt, i < kt.count ? i : kt.count - 1, kFwdKeys, part * kFwdWaves + wave, key_place(i));
+    };
+    auto copy_values = [&](int i, int part) {
+      vals(kt, i < kt.count ? i : kt.count - 1, kFwdKeys, part * kFwdWaves + wave, value_place(i));
+    };
+
+    Row<kHd> st;
+    st.clear();
     f32x16 s[2];
+    bf16x8 pf[2][2];
+    auto score = [&](int i, int b) { s[b] = score_tile<kHd>(key_place(i), 32 * b, qf); };
+    auto values = [&](int i, int b) {
+      const uint32_t vtile = value_place(i);
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      s[b] = score_tile<kHd>(ktile, 32 * b, qf);
-      if (!all) mask_tile(s[b], key0 + 32 * b, p, a.window, a.sinks);
-    }
-    st.raise(half_max(fmaxf(tile_max(s[0]), tile_max(s[1]))) * c2);
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        s[b][j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][j], c2, -st.m));
-        st.l += s[b][j];
-      }
-#pragma unroll
-      for (int step = 0; step < 2; ++step) {
-        const bf16x8 pf = pack_step(s[b], step);
+      for (int step = 0; step < 2; ++step)
 #pragma unroll
         for (int d = 0; d < kHd / 32; ++d)
-          st.o[d] = mfma(col_frag<kHd>(vtile, 32 * b + 16 * step, d), pf, st.o[d]);
+          st.o[d] = mfma(col_frag<kHd>(vtile, 32 * b + 16 * step, d), pf[b][step], st.o[d]);
+    };
+    // exp2 of 32 keys' scores, their sum, and the packed probabilities.
+    auto exps = [&](f32x16 x, int b) {
+      float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        x[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], c2, -st.m));
+        sum[j & 1] += x[j];
+      }
+      st.l += sum[0] + sum[1];
+      pf[b][0] = pack_step(x, 0);
+      pf[b][1] = pack_step(x, 1);
+    };
+    // Mask, maximum and exponentials of tile i.  (Moving exponentials between the
+    // products, one half or all of them, made those turns longer by more: 344 to 426 us
+    // against 289 at 4 x 4096 tokens, 16 and 8 heads of 128.)
+    auto softmax = [&](int i) {
+      const int key0 = kt.key0(i, kFwdKeys);
+      const bool all = key0 + kFwdKeys - 1 <= w_lo && (a.window == 0 || key0 > w_hi - a.window);
+      if (!all) {
+        mask_tile(s[0], key0, p, a.window, a.sinks);
+        mask_tile(s[1], key0 + 32, p, a.window, a.sinks);
+      }
+      st.raise(half_max(fmaxf(tile_max(s[0]), tile_max(s[1]))) * c2);
+      exps(s[0], 0);
+      exps(s[1], 1);
+    };
+
+    arrived(qf);
+    if (kt.count > 0) {
+#pragma unroll
+      for (int part = 0; part < kParts; ++part) {
+        copy_keys(0, part);
+        copy_values(0, part);
+        copy_keys(1, part);
+        copy_values(1, part);
+        copy_keys(2, part);
       }
     }
-  }
-
-  const float l = half_sum(st.l);
-  if (mine < rows) {
-    const float f = l > 0.0f ? 1.0f / l : 0.0f;
-    uint16_t *orow = a.o + (int64_t)qrow * a.os + (int64_t)h * kHd;
+    landed();
+    meet();
+    if (seen > 0) {
+      score(0, 0);
+      score(0, 1);
+      if (!late) softmax(0);
+    }
+    meet();
+    if (late) {
+      if (seen > 0) softmax(0);
+      meet();
+    }
+    int i = 0;
+    for (; i + 1 < seen; ++i) {
+      score(i + 1, 0);
+      copy_keys(i + 3, 0);
+      score(i + 1, 1);
+      copy_values(i + 2, 0);
+      values(i, 0);
+      if (kParts > 1) copy_keys(i + 3, kParts - 1);
+      values(i, 1);
+      if (kParts > 1) copy_values(i + 2, kParts - 1);
+      feed<4, kHd / 8, kHd / 8>();
+      meet();
+      softmax(i + 1);
+      landed();
+      meet();
+    }
+    for (; i < kt.count; ++i) {
+      if (i + 1 == seen) {
+          values(i, 0);
+        values(i, 1);
+      }
 #pragma unroll
-    for (int d = 0; d < kHd / 32; ++d) store_block(orow + 32 * d, st.o[d], f);
-    if (a.lse && half == 0)
-      a.lse[(int64_t)h * a.q_tokens + qrow] = l > 0.0f ? (st.m + __builtin_log2f(l)) * kLn2 : -__builtin_inff();
+      for (int part = 0; part < kParts; ++part) {
+        copy_keys(i + 3, part);
+        copy_values(i + 2, part);
+      }
+      meet();
+      landed();
+      meet();
+    }
+    if (!late) meet();
+
+    const float l = half_sum(st.l);
+    if (mine < rows) {
+      const float f = l > 0.0f ? 1.0f / l : 0.0f;
+      uint16_t *orow = a.o + (int64_t)qrow * a.os + (int64_t)h * kHd;
+#pragma unroll
+      for (int d = 0; d < kHd / 32; ++d) store_block(orow + 32 * d, st.o[d], f);
+      if (a.lse && half == 0)
+        a.lse[(int64_t)h * a.q_tokens + qrow] = l > 0.0f ? (st.m + __builtin_log2f(l)) * kLn2 : -__builtin_inff();
+    }
   }
 }
 
@@ -174,9 +279,9 @@ __device__ __host__ constexpr size_t split_floats() {
 // the waves' states are joined at the end.
 template <int kHd>
 __global__ void __launch_bounds__(64 * kSplitWaves) attn_split_kernel(AttnArgs a, int splits) {
-  constexpr int kTile = kSplitKeys * kHd, kStage = 2 * kTile;
-  constexpr int kCopies = kSplitKeys / kDmaRows<kHd>;
-  __shared__ __attribute__((aligned(1024))) uint16_t lds[kSplitWaves][2][kStage];
+  constexpr int kTile = kTileBytes<kHd>(kSplitKeys), kStage = 2 * kTile;
+  constexpr int kCopies = kSplitKeys / kGroupRows<kHd>;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kSplitWaves][2 * kStage];
   __shared__ float stat[kSplitWaves][2][kSplitRows];
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -207,21 +312,21 @@ __global__ void __launch_bounds__(64 * kSplitWaves) attn_split_kernel(AttnArgs a
   const uint32_t lds0 = lds_addr(lds[wave]);
   auto copy = [&](int i, int buf) {
     const int key0 = kt.key0(i, kSplitKeys);
-    const uint32_t at = lds0 + (uint32_t)(buf * kStage * 2);
+    const uint32_t at = lds0 + (uint32_t)(buf * kStage);
 #pragma unroll
-    for (int c = 0; c < kCopies; ++c)
-      copy_rows<kHd>(at, c * kDmaRows<kHd>, [&](int x) { return kbase + (int64_t)kt.row(key0 + x) * a.ks; });
+    for (int g = 0; g < kCopies; ++g)
+      copy_group<kHd>(at, g, [&](int x) { return kbase + (int64_t)kt.row(key0 + x) * a.ks; });
 #pragma unroll
-    for (int c = 0; c < kCopies; ++c)
-      copy_rows<kHd>(at + kTile * 2, c * kDmaRows<kHd>,
-                     [&](int x) { return vbase + (int64_t)kt.row(key0 + x) * a.vs; });
+    for (int g = 0; g < kCopies; ++g)
+      copy_group<kHd>(at + kTile, g, [&](int x) { return vbase + (int64_t)kt.row(key0 + x) * a.vs; });
   };
 
   Row<kHd> st;
   st.clear();
   const float c2 = a.scale * kLog2e;
   const int begin = (int)((int64_t)kt.count * split / splits), end = (int)((int64_t)kt.count * (split + 1) / splits);
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");    // only copies are counted from here on
+  arrived(qf);                                        // only copies are counted from here on
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   int i = begin + wave;
   if (i < end) copy(i, 0);
   for (int buf = 0; i < end; i += kSplitWaves, buf ^= 1) {
@@ -236,9 +341,8 @@ __global__ void __launch_bounds__(64 * kSplitWaves) attn_split_kernel(AttnArgs a
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
     const int key0 = kt.key0(i, kSplitKeys);
-    const uint32_t ktile = lds0 + (uint32_t)(buf * kStage * 2), vtile = ktile + kTile * 2;
-    const bool all = key0 + kSplitKeys - 1 <= p_lo &&
-                     (a.window == 0 || key0 > p_hi - a.window || key0 + kSplitKeys <= a.sinks);
+    const uint32_t ktile = lds0 + (uint32_t)(buf * kStage), vtile = ktile + kTile;
+    const bool all = key0 + kSplitKeys - 1 <= p_lo && (a.window == 0 || key0 > p_hi - a.window);
     f32x16 s = score_tile<kHd>(ktile, 0, qf);
     if (!all) mask_tile(s, key0, p, a.window, a.sinks);
     st.raise(half_max(tile_max(s)) * c2);
@@ -353,7 +457,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int splits) 
 template <int kHd>
 hipError_t launch(const AttnArgs &a, const AttnPlan &plan, hipStream_t stream) {
   if (!plan.split) {
-    attn_kernel<kHd><<<dim3((unsigned)((int64_t)plan.slots * a.q_heads)), dim3(64 * kFwdWaves), 0, stream>>>(a, plan.slots);
+    attn_kernel<kHd><<<dim3((unsigned)((int64_t)plan.slots * a.q_heads)), dim3(64 * kFwdWaves), 0, stream>>>(a, plan.slots, plan.fold);
     return hipGetLastError();
   }
   attn_split_kernel<kHd><<<dim3((unsigned)((int64_t)plan.slots * a.k_heads * plan.splits)), dim3(64 * kSplitWaves), 0,
@@ -373,9 +477,10 @@ AttnPlan plan_attention(const puro_attention_shape &a) {
   AttnPlan p{};
   p.splits = 1;
   const int64_t group = a.q_heads / a.k_heads;
-  const int64_t big = a.q_tokens / kFwdRows + a.sequences;
+  p.fold = a.window > 0 ? 1 : 2;
+  const int64_t big = a.q_tokens / (kFwdRows * p.fold) + a.sequences;
   const int64_t few = a.q_tokens * group / kSplitRows + a.sequences;
-  p.split = big * a.q_heads < 256;
+  p.split = big * a.q_heads < 128;
   p.slots = (int)(p.split ? few : big);
   if (p.split) {
     // Enough workgroups for the 256 compute units twice over, but at least 8 chunks of

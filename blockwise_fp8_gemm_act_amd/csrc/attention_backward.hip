@@ -21,8 +21,8 @@ constexpr int kDqWaves = 4, kDqRows = 32 * kDqWaves, kDqKeys = 64;
 // row that sees nothing: its P are then 0) and stats[1][h][row] = D.
 template <int kHd>
 __global__ void __launch_bounds__(64 * kDqWaves, 2) attn_dq_kernel(AttnArgs a, int slots) {
-  constexpr int kTile = kDqKeys * kHd;
-  __shared__ __attribute__((aligned(1024))) uint16_t lds[2][2][kTile];
+  constexpr int kTile = kTileBytes<kHd>(kDqKeys);
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2][2][kTile];
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int hk = (int)(blockIdx.x % a.k_heads);
@@ -64,15 +64,17 @@ __global__ void __launch_bounds__(64 * kDqWaves, 2) attn_dq_kernel(AttnArgs a, i
   const uint32_t lds0 = lds_addr(lds);
   auto copy = [&](int i, int buf) {
     const int key0 = kt.key0(i, kDqKeys);
-    const uint32_t at = lds0 + (uint32_t)(buf * 2 * kTile * 2);
+    const uint32_t at = lds0 + (uint32_t)(buf * 2 * kTile);
 #pragma unroll
-    for (int c = wave; c < kDqKeys / kDmaRows<kHd>; c += kDqWaves) {
-      copy_rows<kHd>(at, c * kDmaRows<kHd>, [&](int r) { return kbase + (int64_t)kt.row(key0 + r) * a.ks; });
-      copy_rows<kHd>(at + kTile * 2, c * kDmaRows<kHd>,
+    for (int g = wave; g < kDqKeys / kGroupRows<kHd>; g += kDqWaves) {
+      copy_group<kHd>(at, g, [&](int r) { return kbase + (int64_t)kt.row(key0 + r) * a.ks; });
+      copy_group<kHd>(at + kTile, g,
                      [&](int r) { return vbase + (int64_t)kt.row(key0 + r) * a.vs; });
     }
   };
 
+  arrived(qf);
+  arrived(df);
   f32x16 acc[kHd / 32];
 #pragma unroll
   for (int d = 0; d < kHd / 32; ++d) acc[d] = (f32x16){};
@@ -82,7 +84,7 @@ __global__ void __launch_bounds__(64 * kDqWaves, 2) attn_dq_kernel(AttnArgs a, i
     wait_all_and_meet();
     if (i + 1 < kt.count) copy(i + 1, (i + 1) & 1);
     const int key0 = kt.key0(i, kDqKeys);
-    const uint32_t ktile = lds0 + (uint32_t)((i & 1) * 2 * kTile * 2), vtile = ktile + kTile * 2;
+    const uint32_t ktile = lds0 + (uint32_t)((i & 1) * 2 * kTile), vtile = ktile + kTile;
     const bool none = key0 > w_hi || (a.window > 0 && key0 + kDqKeys - 1 <= w_lo - a.window && key0 >= a.sinks);
     if (none) continue;
     const bool all = key0 + kDqKeys - 1 <= w_lo &&
@@ -152,8 +154,8 @@ __device__ __forceinline__ void dma4(const void *src, uint32_t lds) {
 
 template <int kHd>
 __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a, DkPlan plan) {
-  constexpr int kTile = kDkQueries * kHd;
-  __shared__ __attribute__((aligned(1024))) uint16_t lds[2][2][kTile];
+  constexpr int kTile = kTileBytes<kHd>(kDkQueries);
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2][2][kTile];
   __shared__ __attribute__((aligned(1024))) float stat[2][2][kDkQueries];
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -219,19 +221,21 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
   auto copy = [&](int i, int buf) {
     const int h = hk * a.group + i / tiles;
     const int q0 = (tile0 + i % tiles) * kDkQueries;
-    const uint32_t at = lds0 + (uint32_t)(buf * 2 * kTile * 2);
+    const uint32_t at = lds0 + (uint32_t)(buf * 2 * kTile);
     auto row = [&](int r) { return (int64_t)(sq.q0 + (q0 + r < sq.ql ? q0 + r : sq.ql - 1)); };
     const uint16_t *qb = a.q + (int64_t)h * kHd, *db = a.d_o + (int64_t)h * kHd;
 #pragma unroll
-    for (int c = wave; c < kDkQueries / kDmaRows<kHd>; c += kDkWaves) {
-      copy_rows<kHd>(at, c * kDmaRows<kHd>, [&](int r) { return qb + row(r) * a.qs; });
-      copy_rows<kHd>(at + kTile * 2, c * kDmaRows<kHd>, [&](int r) { return db + row(r) * a.os; });
+    for (int g = wave; g < kDkQueries / kGroupRows<kHd>; g += kDkWaves) {
+      copy_group<kHd>(at, g, [&](int r) { return qb + row(r) * a.qs; });
+      copy_group<kHd>(at + kTile, g, [&](int r) { return db + row(r) * a.os; });
     }
     if (wave < 2)
       dma4(a.ws + (int64_t)(wave * a.q_heads + h) * a.q_tokens + row(lane),
            __builtin_amdgcn_readfirstlane(stat0 + (uint32_t)((buf * 2 + wave) * kDkQueries * 4)));
   };
 
+  arrived(kf);
+  arrived(vf);
   f32x16 dk[kHd / 32], dv[kHd / 32];
 #pragma unroll
   for (int d = 0; d < kHd / 32; ++d) dk[d] = dv[d] = (f32x16){};
@@ -242,7 +246,7 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
     wait_all_and_meet();
     if (i + 1 < end) copy(i + 1, buf ^ 1);
     const int q0 = (tile0 + i % tiles) * kDkQueries;
-    const uint32_t qtile = lds0 + (uint32_t)(buf * 2 * kTile * 2), dtile = qtile + kTile * 2;
+    const uint32_t qtile = lds0 + (uint32_t)(buf * 2 * kTile), dtile = qtile + kTile;
 #pragma unroll 1
     for (int b = 0; b < 2; ++b) {
       const int p_lo = shift + q0 + 32 * b, p_hi = p_lo + 31;

@@ -38,6 +38,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
 }
 
+// Fragments that stay in registers through a loop: waits for their loads here, so that
+// the compiler does not wait for them inside the loop, where its wait would also be one
+// for the copies under way.
+template <int n>
+__device__ __forceinline__ void arrived(bf16x8 (&f)[n]) {
+#pragma unroll
+  for (int i = 0; i < n; ++i) asm volatile("" : "+v"(f[i]));
+}
+
 // The other half wave's value: lanes 0-31 and 32-63 exchange.
 __device__ __forceinline__ float half_max(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -118,15 +127,22 @@ __device__ __forceinline__ KeyTiles key_tiles(int p_lo, int p_hi, int window, in
 }
 
 // ---------------------------------------------------------------- LDS tiles
-// A tile holds rows of kHd bf16; the 16-byte chunk c of row r sits at c ^ swz(r).
-// Row fragments (32 rows, one chunk) are read 16 lanes at a time, transposed
-// fragments as 4 rows by 64 bytes; over the 64 banks with their bit-8 hash both
-// touch every bank once under these swizzles.
+// A tile holds rows of kHd bf16 in groups of 1 KB (4 rows of 128 columns, or 8 of
+// 64), each one copy of a wave, 16 bytes between groups.  Inside a group 4 rows by 64
+// bytes are contiguous: chunk c (16 bytes) of row r of 4 lies at 256 (c/4) + 64 r + 16
+// (c%4); with 64 columns the second 4 rows follow at 512 with the halves of their 64
+// bytes swapped.  Then
+//   - a row fragment (16 rows, one chunk, per phase) touches all 64 banks once, or
+//     nearly: the 4 rows of a block lie 64 bytes apart, the blocks 16 or 32;
+//   - a transposed fragment (4 rows by 64 bytes) is 256 contiguous bytes;
+//   - every address is one lane-dependent base plus a constant, so that the reads
+//     cost no address arithmetic (an xor swizzle took 24 registers or as many
+//     instructions a tile).
 template <int kHd>
-__device__ __forceinline__ int swz(int r) {
-  if (kHd == 128) return ((r & 3) << 2) | ((r >> 2) & 3);
-  return ((r & 2) << 1) | ((r >> 1) & 2) | ((r >> 3) & 1);
-}
+constexpr int kGroupRows = 512 / kHd;
+constexpr int kGroupBytes = 1024 + 16;
+template <int kHd>
+constexpr int kTileBytes(int rows) { return rows / kGroupRows<kHd> * kGroupBytes; }
 
 // Global -> LDS copy of 16 bytes a lane to lds + 16 lane.  Asm, so that the
 // compiler does not make every later LDS read wait for it: completion is awaited
@@ -144,34 +160,88 @@ __device__ __forceinline__ void dma16(const void *src, uint32_t lds) {
       : "memory");
 }
 
+// The same from a uniform base and a 32-bit offset of the lane.  Without a memory
+// clobber, so that reads of other tiles may be scheduled around it: what it writes is
+// read only after a barrier that has one, and what it overwrites was read before one.
+__device__ __forceinline__ void dma16_s(const void *base, uint32_t off, uint32_t lds) {
+  uint32_t save;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %3\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, %2\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(save)
+      : "v"(off), "s"(base), "s"(lds));
+}
+
 __device__ __forceinline__ uint32_t lds_addr(const void *p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
 }
 
-// One 1 KB copy: kRows rows of a tile starting at row r0 (a multiple of kRows);
-// src_row(r) gives the global row that tile row r holds, as a pointer.
+// The row of a group and the 16-byte chunk of it that this lane copies.
 template <int kHd>
-constexpr int kDmaRows = 512 / kHd;    // rows of one copy: 4 or 8
-
-template <int kHd, typename F>
-__device__ __forceinline__ void copy_rows(uint32_t tile, int r0, F src_row) {
+__device__ __forceinline__ void copy_place(int &r, int &c) {
   const int lane = threadIdx.x & 63;
-  const int r = r0 + lane / (kHd / 8), c = lane % (kHd / 8);
-  const uint16_t *p = src_row(r) + 8 * (c ^ swz<kHd>(r));
-  dma16(p, __builtin_amdgcn_readfirstlane(tile + (uint32_t)r0 * kHd * 2));
+  if (kHd == 128) {
+    r = (lane >> 2) & 3;
+    c = 4 * (lane >> 4) + (lane & 3);
+  } else {
+    r = ((lane >> 2) & 3) + 4 * (lane >> 5);
+    c = 4 * ((lane >> 4) & 1) + ((lane & 3) ^ (2 * (lane >> 5)));
+  }
 }
+
+// Copies group g of a tile; src_row(r) gives the global row that tile row r holds.
+template <int kHd, typename F>
+__device__ __forceinline__ void copy_group(uint32_t tile, int g, F src_row) {
+  int r, c;
+  copy_place<kHd>(r, c);
+  dma16(src_row(g * kGroupRows<kHd> + r) + 8 * c,
+        __builtin_amdgcn_readfirstlane(tile + (uint32_t)(g * kGroupBytes)));
+}
+
+// Copies of key (or value) tiles of `unit` keys, group by group and without branches:
+// the base is uniform, a lane's offset inside the tile clamps the rows that no query of
+// the block sees (token strides are below 2^23 elements, so 64 rows fit 32 bits).
+template <int kHd>
+struct TileCopy {
+  const uint16_t *base;
+  int64_t stride;
+  int row;               // this lane's row and chunk of a group
+  uint32_t chunk;
+  __device__ __forceinline__ TileCopy(const uint16_t *base, int64_t stride) : base(base), stride(stride) {
+    int c;
+    copy_place<kHd>(row, c);
+    chunk = (uint32_t)(c * 16);
+  }
+  __device__ __forceinline__ void operator()(const KeyTiles &kt, int i, int unit, int g, uint32_t tile) const {
+    const int key0 = kt.key0(i, unit);
+    const bool first = i < kt.first_n;
+    const int key = key0 + g * kGroupRows<kHd> + row;
+    const int in = key < kt.sinks ? key : clampi(key, first ? 0 : kt.lo, first ? kt.sinks - 1 : kt.hi);
+    dma16_s(base + (int64_t)key0 * stride, (uint32_t)(in - key0) * (uint32_t)(stride * 2) + chunk,
+            tile + (uint32_t)(g * kGroupBytes));
+  }
+};
 
 typedef __attribute__((address_space(3))) bf16x8 lds_bf16x8;
 typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
 
-// Rows r0 .. r0+31, contraction step kk (16 columns): lane l gets row r0 + (l & 31),
-// columns 16 kk + 8 (l / 32) .. +7.
+// Rows r0 .. r0+31 (r0 a multiple of 32), contraction step kk (16 columns): lane l
+// gets row r0 + (l & 31), columns 16 kk + 8 (l / 32) .. +7.
 template <int kHd>
 __device__ __forceinline__ bf16x8 row_frag(uint32_t tile, int r0, int kk) {
   const int lane = threadIdx.x & 63;
   const int r = lane & 31;
-  const uint32_t at = tile + (uint32_t)(r * kHd * 2) + (uint32_t)(((2 * kk + (lane >> 5)) ^ swz<kHd>(r)) * 16);
-  return *(lds_bf16x8 *)(uintptr_t)(at + (uint32_t)(r0 * kHd * 2));
+  uint32_t base = (uint32_t)(r / kGroupRows<kHd> * kGroupBytes + (r & 3) * 64 + (lane >> 5) * 16);
+  uint32_t step = (uint32_t)((kk & 1) * 32);
+  if (kHd == 64) {
+    const uint32_t swap = (uint32_t)((r >> 2) & 1);
+    base += swap * 512;
+    step = (kk & 1) ? 32 - 32 * swap : 32 * swap;
+  }
+  return *(lds_bf16x8 *)(uintptr_t)(tile + base + step + (uint32_t)((kk >> 1) * 256 + kTileBytes<kHd>(r0)));
 }
 
 // The transpose's fragment: lane l gets column 32 db + (l & 31) of the 8 rows r0 +
@@ -181,15 +251,34 @@ template <int kHd>
 __device__ __forceinline__ bf16x8 col_frag(uint32_t tile, int r0, int db) {
   const int lane = threadIdx.x & 63;
   const int half = lane >> 5, i = lane & 15;
-  const int col = 32 * db + (lane & 16) + 4 * (i & 3);
+  uint32_t base = (uint32_t)((i >> 2) * 64 + (i & 3) * 8);
+  if (kHd == 128)
+    base += (uint32_t)(half * kGroupBytes + (lane & 16) * 2);
+  else
+    base += (uint32_t)(half * 512 + ((lane & 16) * 2 ^ half * 32));
   bf16x4 v[2];
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const int r = 4 * half + 8 * w + (i >> 2);
-    const uint32_t at = tile + (uint32_t)(r * kHd * 2) + (uint32_t)(((col >> 3) ^ swz<kHd>(r)) * 16 + (col & 7) * 2);
-    v[w] = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4 *)(uintptr_t)(at + (uint32_t)(r0 * kHd * 2)));
-  }
+  for (int w = 0; w < 2; ++w)
+    v[w] = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+        (lds_bf16x4 *)(uintptr_t)(tile + base + (uint32_t)(db * 256 + kTileBytes<kHd>(r0 + 8 * w))));
   return __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Order of a block of products: the LDS reads of the first `ahead` products go out
+// first, then each product is followed by the reads of one further on (one a product
+// of row fragments, two of column fragments; `rows` products of the first kind come
+// first).  Left alone, the compiler reads, waits and multiplies one by one.
+template <int kAhead, int kRowProducts, int kColProducts>
+__device__ __forceinline__ void feed() {
+  constexpr int n = kRowProducts + kColProducts;
+#pragma unroll
+  for (int j = 0; j < n + kAhead; ++j) {
+    if (j >= kAhead) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if (j < n) {
+      if (j < kRowProducts) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      else __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+    }
+  }
 }
 
 // Registers 8s .. 8s+7 of a score tile as the B operand of step s.

@@ -21,7 +21,7 @@
  *   - Head tensors are [tokens][heads][head_dim] with the heads of a token
  *     densely packed and a free distance between tokens, the `stride` that goes
  *     with each pointer: in elements, a multiple of 8, at least heads *
- *     head_dim.  Slices of a projection's output (its query, key and value
+ *     head_dim and below 2^23.  Slices of a projection's output (its query, key and value
  *     columns) are passed as they lie.  Two slices of the same rows do not
  *     overlap when their strides are equal and their columns are apart.
  *   - head_dim is 64 or 128.
