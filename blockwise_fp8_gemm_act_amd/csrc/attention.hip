@@ -19,23 +19,6 @@ __device__ __forceinline__ f32x16 score_tile(uint32_t ktile, int r0, const bf16x
   return s;
 }
 
-// Masks the scores of keys key0 .. key0+31 for the lane's query at p.
-__device__ __forceinline__ void mask_tile(f32x16 &s, int key0, int p, int window, int sinks) {
-  const int half = (threadIdx.x & 63) >> 5;
-  if (key0 < sinks) {                   // first keys that stay visible among them
-#pragma unroll
-    for (int i = 0; i < 16; ++i) s[i] = visible(key0 + 8 * (i / 4) + 4 * half + i % 4, p, window, sinks) ? s[i] : -__builtin_inff();
-    return;
-  }
-  // p - key is negative for keys after p: causality and the window are one unsigned
-  // comparison.
-  int before = p - key0 - 4 * half;
-  asm volatile("" : "+v"(before));      // keeps the comparisons inside the caller's branch
-  const uint32_t reach = window == 0 ? 0x7fffffffu : (uint32_t)window;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) s[i] = (uint32_t)(before - (8 * (i / 4) + i % 4)) < reach ? s[i] : -__builtin_inff();
-}
-
 // Softmax state of one query (of a lane and its partner): m is the maximum in use,
 // in units of log2, l this lane's share of the sum.
 template <int kHd>

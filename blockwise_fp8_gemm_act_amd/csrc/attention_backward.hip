@@ -59,17 +59,15 @@ __global__ void __launch_bounds__(64 * kDqWaves, 2) attn_dq_kernel(AttnArgs a, i
     a.ws[(int64_t)(a.q_heads + h) * a.q_tokens + qrow] = dd;
   }
 
-  const uint16_t *kbase = a.k + (int64_t)sq.k0 * a.ks + (int64_t)hk * kHd;
-  const uint16_t *vbase = a.v + (int64_t)sq.k0 * a.vs + (int64_t)hk * kHd;
+  const TileCopy<kHd> keys(a.k + (int64_t)sq.k0 * a.ks + (int64_t)hk * kHd, a.ks);
+  const TileCopy<kHd> vals(a.v + (int64_t)sq.k0 * a.vs + (int64_t)hk * kHd, a.vs);
   const uint32_t lds0 = lds_addr(lds);
   auto copy = [&](int i, int buf) {
-    const int key0 = kt.key0(i, kDqKeys);
     const uint32_t at = lds0 + (uint32_t)(buf * 2 * kTile);
 #pragma unroll
     for (int g = wave; g < kDqKeys / kGroupRows<kHd>; g += kDqWaves) {
-      copy_group<kHd>(at, g, [&](int r) { return kbase + (int64_t)kt.row(key0 + r) * a.ks; });
-      copy_group<kHd>(at + kTile, g,
-                     [&](int r) { return vbase + (int64_t)kt.row(key0 + r) * a.vs; });
+      keys(kt, i, kDqKeys, g, at);
+      vals(kt, i, kDqKeys, g, at + kTile);
     }
   };
 
@@ -87,8 +85,7 @@ __global__ void __launch_bounds__(64 * kDqWaves, 2) attn_dq_kernel(AttnArgs a, i
     const uint32_t ktile = lds0 + (uint32_t)((i & 1) * 2 * kTile), vtile = ktile + kTile;
     const bool none = key0 > w_hi || (a.window > 0 && key0 + kDqKeys - 1 <= w_lo - a.window && key0 >= a.sinks);
     if (none) continue;
-    const bool all = key0 + kDqKeys - 1 <= w_lo &&
-                     (a.window == 0 || key0 > w_hi - a.window || key0 + kDqKeys <= a.sinks);
+    const bool all = key0 + kDqKeys - 1 <= w_lo && (a.window == 0 || key0 > w_hi - a.window);
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       f32x16 s = {}, dp = {};
@@ -96,18 +93,17 @@ __global__ void __launch_bounds__(64 * kDqWaves, 2) attn_dq_kernel(AttnArgs a, i
       for (int kk = 0; kk < kHd / 16; ++kk) s = mfma(row_frag<kHd>(ktile, 32 * b, kk), qf[kk], s);
 #pragma unroll
       for (int kk = 0; kk < kHd / 16; ++kk) dp = mfma(row_frag<kHd>(vtile, 32 * b, kk), df[kk], dp);
+      feed<2, kHd / 8, 0>();
+      if (!all) mask_tile(s, key0 + 32 * b, p, a.window, a.sinks);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], c2, -lse2));
-        if (!all) e = visible(key0 + 32 * b + 8 * (j / 4) + 4 * half + j % 4, p, a.window, a.sinks) ? e : 0.0f;
-        s[j] = e * (dp[j] - dd);
-      }
+      for (int j = 0; j < 16; ++j) s[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], c2, -lse2)) * (dp[j] - dd);
 #pragma unroll
       for (int step = 0; step < 2; ++step) {
         const bf16x8 sf = pack_step(s, step);
 #pragma unroll
         for (int d = 0; d < kHd / 32; ++d) acc[d] = mfma(col_frag<kHd>(ktile, 32 * b + 16 * step, d), sf, acc[d]);
       }
+      feed<2, 0, kHd / 16>();
     }
   }
   if (mine < rows) {
@@ -120,19 +116,53 @@ __global__ void __launch_bounds__(64 * kDqWaves, 2) attn_dq_kernel(AttnArgs a, i
 // ---------------------------------------------------------------- dk, dv
 constexpr int kDkWaves = 4, kDkRows = 32 * kDkWaves, kDkQueries = 64;
 
-// Work of one block of 128 keys and one key head: tiles of 64 queries of each head
-// of the group.  `near` tiles are those whose queries have the block in their
-// window; where the block holds first keys, `far` tiles are those past it, which
-// see the first keys only.  Both are cut into parts, so that a long walk (many
-// heads, few keys; first keys under a long sequence) is shared by workgroups, which
-// then leave fp32 partials for the join.
+// Work on one block of 128 keys and one key head: tiles of 64 queries of each head of
+// the group.  `near` tiles hold the queries that have the block in their window; for a
+// block of first keys `far` tiles hold the later queries, which see the first keys
+// only.  Without far work such a block would walk its whole sequence while all others
+// walk a window.  Either walk is cut into parts where it is long for the card (many
+// heads over few keys; a long sequence past its first keys), which leave fp32 partials
+// for the join.
 struct DkPlan {
   int slots;          // key blocks, empty ones included
-  int parts;          // of the near tiles
+  int parts;          // of each near walk
   int far_blocks;     // key blocks of a sequence that hold first keys; 0: no far work
-  int far_parts;
-  size_t near_at, far_at, floats;   // partials in the workspace (floats from its start)
+  int far_slots;      // parts of far walks over all sequences, empty ones included
+  size_t near_at, edge_at, far_at, floats;   // partials in the workspace, in floats: of near walks, of near walks over
+                                             // first keys that are not cut, of far walks
 };
+constexpr int kFarChunk = 16;     // tiles of a far part
+
+struct Walk {
+  int q_lo, q_hi;     // queries of the sequence
+  int tile0, tiles;
+};
+__device__ __forceinline__ Walk walk_of(const AttnArgs &a, const DkPlan &plan, const Seq &sq, int slot, bool far) {
+  const int key0 = slot * kDkRows, shift = sq.kl - sq.ql;
+  const int keys = sq.kl - key0 < kDkRows ? sq.kl - key0 : kDkRows;
+  Walk w{key0 - shift, sq.ql - 1, 0, 0};
+  const bool windowed = a.window > 0 && (key0 >= a.sinks || slot < plan.far_blocks);
+  const int near = windowed ? key0 + keys - 1 + a.window - 1 - shift : w.q_hi;   // last query with the block in its window
+  if (far) w.q_lo = near + 1 > w.q_lo ? near + 1 : w.q_lo;
+  else if (near < w.q_hi) w.q_hi = near;
+  if (w.q_lo < 0) w.q_lo = 0;
+  w.tile0 = w.q_lo / kDkQueries;
+  w.tiles = w.q_lo <= w.q_hi ? w.q_hi / kDkQueries - w.tile0 + 1 : 0;
+  return w;
+}
+
+// Far parts are numbered over the sequences like query tiles of kFarChunk * 64 / group
+// rows; a sequence uses as many of its numbers as its far walk has chunks.
+__device__ __forceinline__ int far_first(const AttnArgs &a, int s) {
+  const int start = a.q_start ? clampi(a.q_start[s], 0, a.q_tokens) : (s == 0 ? 0 : a.q_tokens);
+  return (int)((int64_t)start * a.group / (kFarChunk * kDkQueries)) + s;
+}
+__device__ __forceinline__ int far_parts(const AttnArgs &a, const DkPlan &plan, const Seq &sq, int s, int slot) {
+  const Walk w = walk_of(a, plan, sq, slot, true);
+  const int64_t chunks = ((int64_t)w.tiles * a.group + kFarChunk - 1) / kFarChunk;
+  const int room = far_first(a, s + 1) - far_first(a, s);
+  return (int)(chunks < room ? chunks : (room > 0 ? room : 0));
+}
 
 template <int kHd>
 __host__ __device__ constexpr size_t part_floats() {
@@ -161,47 +191,39 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int hk = (int)(blockIdx.x % a.k_heads);
   int rest = (int)(blockIdx.x / a.k_heads);
-  const int far_items = a.sequences * plan.far_blocks * plan.far_parts;
+  const int far_items = plan.far_slots * plan.far_blocks;
   const bool far = rest < far_items;
   int part, parts, slot, s;
-  float *partial = nullptr;
   if (far) {
-    part = rest % plan.far_parts;
-    parts = plan.far_parts;
-    s = rest / plan.far_parts / plan.far_blocks;
-    slot = rest / plan.far_parts % plan.far_blocks;
-    partial = a.ws + plan.far_at +
-              ((size_t)((s * plan.far_blocks + slot) * a.k_heads + hk) * (plan.far_parts + 1) + part) * part_floats<kHd>();
+    slot = rest % plan.far_blocks;
+    part = rest / plan.far_blocks;
+    s = find_seq(a.q_start, a.sequences, a.q_tokens, a.group, kFarChunk * kDkQueries, part);
+    parts = 1;
   } else {
     rest -= far_items;
     part = rest % plan.parts;
     parts = plan.parts;
     slot = rest / plan.parts;
-    const int number = slot;
     s = find_seq(a.k_start, a.sequences, a.k_tokens, 1, kDkRows, slot);
-    if (parts > 1)
-      partial = a.ws + plan.near_at + ((size_t)(number * a.k_heads + hk) * parts + part) * part_floats<kHd>();
-    else if (slot < plan.far_blocks)
-      partial = a.ws + plan.far_at +
-                ((size_t)((s * plan.far_blocks + slot) * a.k_heads + hk) * (plan.far_parts + 1) + plan.far_parts) *
-                    part_floats<kHd>();
   }
   const Seq sq = load_seq(a, s);
   if ((int64_t)slot * kDkRows >= sq.kl) return;
+  const int fars = slot < plan.far_blocks ? far_parts(a, plan, sq, s, slot) : 0;
+  float *partial = nullptr;
+  if (far) {
+    if (part >= fars) return;
+    parts = fars;
+    partial = a.ws + plan.far_at + (size_t)(blockIdx.x) * part_floats<kHd>();
+  } else if (parts > 1) {
+    partial = a.ws + plan.near_at + ((size_t)(rest / parts * a.k_heads + hk) * parts + part) * part_floats<kHd>();
+  } else if (fars > 0) {
+    partial = a.ws + plan.edge_at + (size_t)((s * plan.far_blocks + slot) * a.k_heads + hk) * part_floats<kHd>();
+  }
   const int key0 = slot * kDkRows;
   const int keys = sq.kl - key0 < kDkRows ? sq.kl - key0 : kDkRows;
   const int shift = sq.kl - sq.ql;
-
-  // Queries (as numbers in the sequence) that this work sees.
-  int q_lo = key0 - shift, q_hi = sq.ql - 1;
-  // The last query with the block in its window; without far work first keys are seen to the end.
-  const bool windowed = a.window > 0 && (key0 >= a.sinks || slot < plan.far_blocks);
-  const int q_near = windowed ? key0 + keys - 1 + a.window - 1 - shift : q_hi;
-  if (far) q_lo = q_near + 1 > q_lo ? q_near + 1 : q_lo;
-  else if (q_near < q_hi) q_hi = q_near;
-  if (q_lo < 0) q_lo = 0;
-  const int tile0 = q_lo / kDkQueries;
-  const int tiles = q_lo <= q_hi ? q_hi / kDkQueries - tile0 + 1 : 0;
+  const Walk walk = walk_of(a, plan, sq, slot, far);
+  const int tile0 = walk.tile0, tiles = walk.tiles;
   const int64_t work = (int64_t)tiles * a.group;
   const int begin = (int)(work * part / parts), end = (int)(work * (part + 1) / parts);
 
@@ -209,6 +231,11 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
   const int krow = sq.k0 + key0 + (mine < keys ? mine : keys - 1);
   const int key = key0 + mine;
   const int w_lo = key0 + 32 * wave, w_hi = w_lo + 31;
+  // The positions that see this lane's key in this work: seen_n of them from seen_lo.
+  const int first = shift + walk.q_lo, final = shift + walk.q_hi;
+  const int seen_lo = key > first ? key : first;
+  const int seen_hi = a.window == 0 || key < a.sinks || key + a.window - 1 > final ? final : key + a.window - 1;
+  const uint32_t seen_n = (uint32_t)(seen_hi >= seen_lo ? seen_hi - seen_lo + 1 : 0);
   bf16x8 kf[kHd / 16], vf[kHd / 16];
 #pragma unroll
   for (int kk = 0; kk < kHd / 16; ++kk) {
@@ -218,19 +245,24 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
   }
 
   const uint32_t lds0 = lds_addr(lds), stat0 = lds_addr(stat);
+  int copy_r, copy_c;
+  copy_place<kHd>(copy_r, copy_c);
   auto copy = [&](int i, int buf) {
     const int h = hk * a.group + i / tiles;
     const int q0 = (tile0 + i % tiles) * kDkQueries;
     const uint32_t at = lds0 + (uint32_t)(buf * 2 * kTile);
-    auto row = [&](int r) { return (int64_t)(sq.q0 + (q0 + r < sq.ql ? q0 + r : sq.ql - 1)); };
-    const uint16_t *qb = a.q + (int64_t)h * kHd, *db = a.d_o + (int64_t)h * kHd;
+    const int last = sq.ql - 1 - q0;                     // rows past the sequence's end: its last one
+    const uint16_t *qb = a.q + (int64_t)(sq.q0 + q0) * a.qs + (int64_t)h * kHd;
+    const uint16_t *db = a.d_o + (int64_t)(sq.q0 + q0) * a.os + (int64_t)h * kHd;
 #pragma unroll
     for (int g = wave; g < kDkQueries / kGroupRows<kHd>; g += kDkWaves) {
-      copy_group<kHd>(at, g, [&](int r) { return qb + row(r) * a.qs; });
-      copy_group<kHd>(at + kTile, g, [&](int r) { return db + row(r) * a.os; });
+      const int r = g * kGroupRows<kHd> + copy_r;
+      const uint32_t in = (uint32_t)(r < last ? r : last);
+      dma16_s(qb, in * (uint32_t)(a.qs * 2) + copy_c * 16, at + (uint32_t)(g * kGroupBytes));
+      dma16_s(db, in * (uint32_t)(a.os * 2) + copy_c * 16, at + kTile + (uint32_t)(g * kGroupBytes));
     }
     if (wave < 2)
-      dma4(a.ws + (int64_t)(wave * a.q_heads + h) * a.q_tokens + row(lane),
+      dma4(a.ws + (int64_t)(wave * a.q_heads + h) * a.q_tokens + sq.q0 + q0 + (lane < last ? lane : last),
            __builtin_amdgcn_readfirstlane(stat0 + (uint32_t)((buf * 2 + wave) * kDkQueries * 4)));
   };
 
@@ -250,18 +282,24 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
 #pragma unroll 1
     for (int b = 0; b < 2; ++b) {
       const int p_lo = shift + q0 + 32 * b, p_hi = p_lo + 31;
-      // Far work starts inside a tile: queries before it belong to the near work.
-      const int first = far ? shift + q_lo : 0;
-      const bool none = q0 + 32 * b >= sq.ql || w_lo > p_hi || p_hi < first ||
+      const bool none = p_lo > final || p_hi < first || w_lo > p_hi ||
                         (a.window > 0 && w_hi <= p_lo - a.window && w_lo >= a.sinks);
       if (none) continue;
-      const bool all = q0 + 32 * b + 31 < sq.ql && w_hi <= p_lo && p_lo >= first && (far || p_hi <= shift + q_hi) &&
+      const bool all = p_lo >= first && p_hi <= final && w_hi <= p_lo &&
                        (a.window == 0 || w_lo > p_hi - a.window || w_hi < a.sinks);
       f32x16 s = {}, dp = {};
 #pragma unroll
       for (int kk = 0; kk < kHd / 16; ++kk) s = mfma(row_frag<kHd>(qtile, 32 * b, kk), kf[kk], s);
 #pragma unroll
       for (int kk = 0; kk < kHd / 16; ++kk) dp = mfma(row_frag<kHd>(dtile, 32 * b, kk), vf[kk], dp);
+      feed<2, kHd / 8, 0>();
+      if (!all) {
+        int from = p_lo + 4 * half - seen_lo;
+        asm volatile("" : "+v"(from));      // keeps the comparisons inside this branch
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          s[j] = (uint32_t)(from + 8 * (j / 4) + j % 4) < seen_n ? s[j] : -__builtin_inff();
+      }
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const f32x4 lse2 = *reinterpret_cast<const f32x4 *>(&stat[buf][0][32 * b + 8 * g + 4 * half]);
@@ -269,13 +307,8 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int j = 4 * g + e;
-          float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], c2, -lse2[e]));
-          if (!all) {
-            const int qi = q0 + 32 * b + 8 * g + 4 * half + e;
-            x = qi <= q_hi && shift + qi >= first && visible(key, shift + qi, a.window, a.sinks) ? x : 0.0f;
-          }
-          s[j] = x;
-          dp[j] = x * (dp[j] - dd[e]);
+          s[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], c2, -lse2[e]));
+          dp[j] = s[j] * (dp[j] - dd[e]);
         }
       }
 #pragma unroll
@@ -287,6 +320,7 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
           dk[d] = mfma(col_frag<kHd>(qtile, 32 * b + 16 * step, d), sf, dk[d]);
         }
       }
+      feed<2, 0, kHd / 8>();
     }
   }
 
@@ -322,8 +356,8 @@ __global__ void __launch_bounds__(256) attn_dkdv_join_kernel(AttnArgs a, DkPlan 
   int slot = number;
   const int s = find_seq(a.k_start, a.sequences, a.k_tokens, 1, kDkRows, slot);
   const Seq sq = load_seq(a, s);
-  const bool far = slot < plan.far_blocks;
-  if (plan.parts == 1 && !far) return;
+  const int fars = slot < plan.far_blocks && (int64_t)slot * kDkRows < sq.kl ? far_parts(a, plan, sq, s, slot) : 0;
+  if (plan.parts == 1 && fars == 0) return;
   const int r = (rest % kChunks) * kRows + (int)threadIdx.x / kThreads, c = 8 * ((int)threadIdx.x % kThreads);
   if ((int64_t)slot * kDkRows + r >= sq.kl) return;
   float x[2][8] = {};
@@ -340,10 +374,12 @@ __global__ void __launch_bounds__(256) attn_dkdv_join_kernel(AttnArgs a, DkPlan 
   if (plan.parts > 1)
     for (int p = 0; p < plan.parts; ++p)
       add(a.ws + plan.near_at + ((size_t)(number * a.k_heads + hk) * plan.parts + p) * part_floats<kHd>());
-  if (far) {
-    const float *from = a.ws + plan.far_at +
-                        (size_t)((s * plan.far_blocks + slot) * a.k_heads + hk) * (plan.far_parts + 1) * part_floats<kHd>();
-    for (int p = 0; p < plan.far_parts + (plan.parts == 1); ++p) add(from + p * part_floats<kHd>());
+  else
+    add(a.ws + plan.edge_at + (size_t)((s * plan.far_blocks + slot) * a.k_heads + hk) * part_floats<kHd>());
+  if (fars > 0) {
+    const int f0 = far_first(a, s);
+    for (int p = 0; p < fars; ++p)
+      add(a.ws + plan.far_at + (size_t)(((f0 + p) * plan.far_blocks + slot) * a.k_heads + hk) * part_floats<kHd>());
   }
   const int64_t row = sq.k0 + slot * kDkRows + r;
   u32x4 k, v;
@@ -364,26 +400,24 @@ DkPlan plan_dk(int64_t q_tokens, int64_t k_tokens, int64_t sequences, int64_t q_
   p.slots = (int)(k_tokens / kDkRows + sequences);
   const int64_t group = q_heads / k_heads;
   const int64_t per_seq = (q_tokens + sequences - 1) / sequences;
-  // Near tiles of a block, and parts of at least 8 of them where the blocks alone do
-  // not fill the card twice over.
-  int64_t seen = window > 0 && window + kDkRows < per_seq ? window + kDkRows : per_seq;
-  int64_t parts = 512 / ((int64_t)p.slots * k_heads);
-  const int64_t most = seen / kDkQueries * group / 8;
+  // Near walks are cut, into parts of at least 8 tiles, where the blocks alone do not
+  // fill the card's 512 places (256 compute units, two workgroups each) twice.
+  const int64_t seen = window > 0 && window + kDkRows < per_seq ? window + kDkRows : per_seq;
+  int64_t parts = 1024 / ((int64_t)p.slots * k_heads);
+  const int64_t most = (seen + kDkQueries - 1) / kDkQueries * group / 8;
   if (parts > most) parts = most;
   if (parts > 16) parts = 16;
   p.parts = (int)(parts < 1 ? 1 : parts);
-  p.near_at = (size_t)2 * q_heads * q_tokens;
-  p.near_at = (p.near_at + 63) / 64 * 64;
+  p.near_at = ((size_t)2 * q_heads * q_tokens + 63) / 64 * 64;
   p.floats = p.near_at + (p.parts > 1 ? (size_t)p.slots * k_heads * p.parts * floats : 0);
-  p.far_at = p.floats;
-  // Far work pays where a sequence is several windows long; many first keys make
+  p.edge_at = p.far_at = p.floats;
+  // Far work pays where a sequence may be several windows long; many first keys make
   // enough blocks by themselves, and partials for them would be large.
-  int64_t far = per_seq / (window + kDkRows);
-  if (far > 32) far = 32;
-  if (window > 0 && sinks > 0 && sinks <= 2 * kDkRows && far >= 2) {
+  if (window > 0 && sinks > 0 && sinks <= 2 * kDkRows && q_tokens >= 2 * (window + kDkRows)) {
     p.far_blocks = (int)((sinks + kDkRows - 1) / kDkRows);
-    p.far_parts = (int)far;
-    p.floats += (size_t)sequences * p.far_blocks * k_heads * (p.far_parts + 1) * floats;
+    p.far_slots = (int)(q_tokens * group / (kFarChunk * kDkQueries) + sequences);
+    p.far_at = p.edge_at + (p.parts == 1 ? (size_t)sequences * p.far_blocks * k_heads * floats : 0);
+    p.floats = p.far_at + (size_t)p.far_slots * p.far_blocks * k_heads * floats;
   }
   return p;
 }
@@ -397,7 +431,7 @@ hipError_t launch(const AttnArgs &a, hipStream_t stream) {
   }
   if (a.k_tokens == 0) return hipSuccess;
   const DkPlan plan = plan_dk(a.q_tokens, a.k_tokens, a.sequences, a.q_heads, a.k_heads, kHd, a.window, a.sinks);
-  const int64_t items = (int64_t)a.sequences * plan.far_blocks * plan.far_parts + (int64_t)plan.slots * plan.parts;
+  const int64_t items = (int64_t)plan.far_slots * plan.far_blocks + (int64_t)plan.slots * plan.parts;
   attn_dkdv_kernel<kHd><<<dim3((unsigned)(items * a.k_heads)), dim3(64 * kDkWaves), 0, stream>>>(a, plan);
   if (hipError_t e = hipGetLastError()) return e;
   if (plan.parts > 1 || plan.far_blocks > 0) {

@@ -99,10 +99,6 @@ __device__ __forceinline__ int find_seq(const int32_t *start, int sequences, int
 }
 
 // ---------------------------------------------------------------- mask
-__device__ __forceinline__ bool visible(int key, int p, int window, int sinks) {
-  return key <= p && (window == 0 || key > p - window || key < sinks);
-}
-
 // The key tiles that a block of queries at positions p_lo .. p_hi looks at, `unit`
 // keys each: those of the visible first keys, then those of the window.  Keys that
 // none of these queries sees are read from row `lo` or `hi` instead (they are
@@ -287,6 +283,26 @@ __device__ __forceinline__ bf16x8 pack_step(const f32x16 &p, int s) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) w[j] = pack_bf16(p[8 * s + 2 * j], p[8 * s + 2 * j + 1]);
   return __builtin_bit_cast(bf16x8, w);
+}
+
+// Masks the scores of keys key0 .. key0+31 for the lane's query at p.
+__device__ __forceinline__ void mask_tile(f32x16 &s, int key0, int p, int window, int sinks) {
+  const int half = (threadIdx.x & 63) >> 5;
+  if (key0 < sinks) {                   // first keys that stay visible among them
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int key = key0 + 8 * (i / 4) + 4 * half + i % 4;
+      s[i] = (key <= p) & ((window == 0) | (key > p - window) | (key < sinks)) ? s[i] : -__builtin_inff();
+    }
+    return;
+  }
+  // p - key is negative for keys after p: causality and the window are one unsigned
+  // comparison.
+  int before = p - key0 - 4 * half;
+  asm volatile("" : "+v"(before));      // keeps the comparisons inside the caller's branch
+  const uint32_t reach = window == 0 ? 0x7fffffffu : (uint32_t)window;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s[i] = (uint32_t)(before - (8 * (i / 4) + i % 4)) < reach ? s[i] : -__builtin_inff();
 }
 
 // One block of 32 columns of a transposed accumulator (column of the result = lane

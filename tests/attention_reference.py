@@ -75,12 +75,9 @@ def norm_backward(g, x, w, eps):
 
 # ---------------------------------------------------------------- attention
 def mask(ql, kl, window, sinks):
-    m = torch.zeros(ql, kl, dtype=torch.bool)
-    for i in range(ql):
-        p = kl - ql + i
-        for j in range(max(0, min(kl, p + 1))):
-            m[i, j] = window == 0 or j > p - window or j < sinks
-    return m
+    p = torch.arange(ql)[:, None] + (kl - ql)
+    j = torch.arange(kl)[None]
+    return (j <= p) & ((j > p - window) | (j < sinks) if window else torch.ones(1, 1, dtype=torch.bool))
 
 
 def attention(q, k, v, seqs, window=0, sinks=0, scale=None, do=None, bounds=False):

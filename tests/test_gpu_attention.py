@@ -326,3 +326,15 @@ def test_refusals():
     small = torch.empty(64, dtype=torch.uint8, device="cuda")
     with pytest.raises(puro.PuroError):
         puro.attention_backward(q, q, k, v, o, lse, workspace=small)
+
+
+@pytest.mark.parametrize("ql,window,sinks,qh,kh", [([1500, 700], 60, 5, 4, 1), ([2600], 100, 200, 2, 1), ([40] * 30 + [1300], 50, 4, 4, 2)])
+def test_backward_of_first_keys_under_long_sequences(ql, window, sinks, qh, kh):
+    """Walks of first keys cut into several parts, beside sequences that need none."""
+    q, k, v, seqs = packed(ql, ql, qh, kh, 64, 130)
+    do = normal(q.shape, 133, 1e-3)
+    o, lse = puro.attention(q, k, v, starts(ql), starts(ql), window=window, sinks=sinks)
+    got = puro.attention_backward(do, q, k, v, o, lse, starts(ql), starts(ql), window=window, sinks=sinks)
+    want = ref.attention(q, k, v, seqs, window, sinks, do=do, bounds=True)
+    for name, g in zip(("dq", "dk", "dv"), got):
+        ref.check(g, want[name], want["b_" + name], name)
