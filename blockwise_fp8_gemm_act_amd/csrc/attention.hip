@@ -258,13 +258,13 @@ __device__ __host__ constexpr size_t split_floats() {
 
 // A row of a tile is (query, head of the group): rows of a sequence are numbered
 // query * group + head, so that the heads that share keys share the tile.  Each
-// wave keeps its own two stages of keys and values in LDS and waits for nobody;
+// wave keeps its own two places for keys and two for values in LDS and waits for nobody;
 // the waves' states are joined at the end.
 template <int kHd>
 __global__ void __launch_bounds__(64 * kSplitWaves) attn_split_kernel(AttnArgs a, int splits) {
-  constexpr int kTile = kTileBytes<kHd>(kSplitKeys), kStage = 2 * kTile;
+  constexpr int kTile = kTileBytes<kHd>(kSplitKeys);
   constexpr int kCopies = kSplitKeys / kGroupRows<kHd>;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kSplitWaves][2 * kStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kSplitWaves][4 * kTile];
   __shared__ float stat[kSplitWaves][2][kSplitRows];
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -290,18 +290,17 @@ __global__ void __launch_bounds__(64 * kSplitWaves) attn_split_kernel(AttnArgs a
   for (int kk = 0; kk < kHd / 16; ++kk)
     qf[kk] = load8(a.q + (int64_t)qrow * a.qs + (int64_t)h * kHd + 16 * kk + 8 * half);
 
-  const uint16_t *kbase = a.k + (int64_t)sq.k0 * a.ks + (int64_t)hk * kHd;
-  const uint16_t *vbase = a.v + (int64_t)sq.k0 * a.vs + (int64_t)hk * kHd;
+  const TileCopy<kHd> keys(a.k + (int64_t)sq.k0 * a.ks + (int64_t)hk * kHd, a.ks);
+  const TileCopy<kHd> vals(a.v + (int64_t)sq.k0 * a.vs + (int64_t)hk * kHd, a.vs);
   const uint32_t lds0 = lds_addr(lds[wave]);
-  auto copy = [&](int i, int buf) {
-    const int key0 = kt.key0(i, kSplitKeys);
-    const uint32_t at = lds0 + (uint32_t)(buf * kStage);
+  // Chunk i's keys at the places 0 and 1 in turn, its values at 2 and 3.
+  auto copy_keys = [&](int i, int odd) {
 #pragma unroll
-    for (int g = 0; g < kCopies; ++g)
-      copy_group<kHd>(at, g, [&](int x) { return kbase + (int64_t)kt.row(key0 + x) * a.ks; });
+    for (int g = 0; g < kCopies; ++g) keys(kt, i, kSplitKeys, g, lds0 + (uint32_t)(odd * kTile));
+  };
+  auto copy_values = [&](int i, int odd) {
 #pragma unroll
-    for (int g = 0; g < kCopies; ++g)
-      copy_group<kHd>(at + kTile, g, [&](int x) { return vbase + (int64_t)kt.row(key0 + x) * a.vs; });
+    for (int g = 0; g < kCopies; ++g) vals(kt, i, kSplitKeys, g, lds0 + (uint32_t)((2 + odd) * kTile));
   };
 
   Row<kHd> st;
@@ -310,23 +309,36 @@ __global__ void __launch_bounds__(64 * kSplitWaves) attn_split_kernel(AttnArgs a
   const int begin = (int)((int64_t)kt.count * split / splits), end = (int)((int64_t)kt.count * (split + 1) / splits);
   arrived(qf);                                        // only copies are counted from here on
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  // Copies run two chunks ahead, each issued as soon as its place has been read: keys
+  // after the scores, values after their products.  Waiting for one tile then leaves
+  // the three younger ones under way.
+  auto younger = [&](bool three) {
+    if (!three) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    else if (kCopies == 8) asm volatile("s_waitcnt vmcnt(24)" ::: "memory");
+    else asm volatile("s_waitcnt vmcnt(12)" ::: "memory");
+  };
+  auto read = [&]() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
   int i = begin + wave;
-  if (i < end) copy(i, 0);
-  for (int buf = 0; i < end; i += kSplitWaves, buf ^= 1) {
-    // The other buffer's reads are done; once its copies are under way only they may
-    // be outstanding.
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if (i + kSplitWaves < end) {
-      copy(i + kSplitWaves, buf ^ 1);
-      if (kCopies == 8) asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
-      else asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
-    } else {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    }
+  if (i < end) {
+    copy_keys(i, 0);
+    copy_values(i, 0);
+  }
+  if (i + kSplitWaves < end) {
+    copy_keys(i + kSplitWaves, 1);
+    copy_values(i + kSplitWaves, 1);
+  }
+  for (int odd = 0; i < end; i += kSplitWaves, odd ^= 1) {
+    const bool one = i + kSplitWaves < end, two = i + 2 * kSplitWaves < end;    // chunks that follow
     const int key0 = kt.key0(i, kSplitKeys);
-    const uint32_t ktile = lds0 + (uint32_t)(buf * kStage), vtile = ktile + kTile;
-    const bool all = key0 + kSplitKeys - 1 <= p_lo && (a.window == 0 || key0 > p_hi - a.window);
+    const uint32_t ktile = lds0 + (uint32_t)(odd * kTile), vtile = ktile + 2 * kTile;
+    younger(one);
     f32x16 s = score_tile<kHd>(ktile, 0, qf);
+    feed<4, kHd / 16, 0>();
+    if (two) {
+      read();
+      copy_keys(i + 2 * kSplitWaves, odd);
+    }
+    const bool all = key0 + kSplitKeys - 1 <= p_lo && (a.window == 0 || key0 > p_hi - a.window);
     if (!all) mask_tile(s, key0, p, a.window, a.sinks);
     st.raise(half_max(tile_max(s)) * c2);
 #pragma unroll
@@ -334,16 +346,22 @@ __global__ void __launch_bounds__(64 * kSplitWaves) attn_split_kernel(AttnArgs a
       s[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], c2, -st.m));
       st.l += s[j];
     }
+    younger(two);
 #pragma unroll
     for (int step = 0; step < 2; ++step) {
       const bf16x8 pf = pack_step(s, step);
 #pragma unroll
       for (int d = 0; d < kHd / 32; ++d) st.o[d] = mfma(col_frag<kHd>(vtile, 16 * step, d), pf, st.o[d]);
     }
+    feed<4, 0, kHd / 16>();
+    if (two) {
+      read();
+      copy_values(i + 2 * kSplitWaves, odd);
+    }
   }
 
   // Join the waves: each scales its state to the common maximum, wave by wave in
-  // order, through LDS (which the stages no longer need).
+  // order, through LDS (which no copy needs any more).
   const float l = half_sum(st.l);
   if (half == 0) {
     stat[wave][0][mine] = st.m;
@@ -356,7 +374,7 @@ __global__ void __launch_bounds__(64 * kSplitWaves) attn_split_kernel(AttnArgs a
 #pragma unroll
   for (int w = 0; w < kSplitWaves; ++w) sum += stat[w][1][mine] * __builtin_amdgcn_exp2f(stat[w][0][mine] - m);
   const float f = __builtin_amdgcn_exp2f(st.m - m);
-  // Each wave's own stages hold its scaled accumulators, [d][row]: 32 floats a row of
+  // Each wave's own part holds its scaled accumulators, [d][row]: 32 floats a row of
   // d, one bank row for the 32 queries.
   float *acc = reinterpret_cast<float *>(lds[wave]);
 #pragma unroll
@@ -402,10 +420,13 @@ __global__ void __launch_bounds__(64 * kSplitWaves) attn_split_kernel(AttnArgs a
   }
 }
 
-// One wave a row: its lanes take kHd / 64 columns each.
+// One wave a row: lanes first as splits (the maxima and sums of up to 128 of them),
+// then as columns, kHd / 64 each, eight splits' partials in flight.
+constexpr int kMostSplits = 128;
 template <int kHd>
 __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int splits) {
   constexpr int kPer = kHd / 64;
+  typedef float cols __attribute__((ext_vector_type(kPer)));
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int hk = (int)(blockIdx.x % a.k_heads);
@@ -417,15 +438,34 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int splits) 
   const int r = slot * kSplitRows + mine;
   const int qrow = sq.q0 + r / a.group, h = hk * a.group + r % a.group;
   const float *part = a.ws + (size_t)((size_t)tile * a.k_heads + hk) * splits * split_floats<kHd>();
-  float m = kNoMax;
-  for (int s = 0; s < splits; ++s) m = fmaxf(m, part[s * split_floats<kHd>() + kSplitRows * kHd + mine]);
-  float sum = 0.0f, x[kPer] = {};
-  for (int s = 0; s < splits; ++s) {
-    const float *one = part + s * split_floats<kHd>();
-    const float f = __builtin_amdgcn_exp2f(one[kSplitRows * kHd + mine] - m);
-    sum += one[kSplitRows * kHd + kSplitRows + mine] * f;
+  float ms[2], ls[2], m = kNoMax, sum = 0.0f;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) x[j] += one[mine * kHd + kPer * lane + j] * f;
+  for (int w = 0; w < 2; ++w) {
+    const int s = 64 * w + lane;
+    const float *stat = part + (s < splits ? s : 0) * split_floats<kHd>() + kSplitRows * kHd + mine;
+    ms[w] = s < splits ? stat[0] : kNoMax;
+    ls[w] = s < splits ? stat[kSplitRows] : 0.0f;
+  }
+  m = wave_max(fmaxf(ms[0], ms[1]));
+#pragma unroll
+  for (int w = 0; w < 2; ++w) ms[w] = __builtin_amdgcn_exp2f(ms[w] - m);
+  for (int s = 0; s < splits; ++s)      // in order, as the columns below
+    sum += __int_as_float(__builtin_amdgcn_readlane(__float_as_int(s < 64 ? ms[0] * ls[0] : ms[1] * ls[1]), s & 63));
+  float x[kPer] = {};
+  for (int s0 = 0; s0 < splits; s0 += 8) {
+    cols one[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int s = s0 + e < splits ? s0 + e : splits - 1;
+      one[e] = *reinterpret_cast<const cols *>(part + s * split_floats<kHd>() + mine * kHd + kPer * lane);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int s = s0 + e;
+      const float f = s < splits ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(s < 64 ? ms[0] : ms[1]), s & 63)) : 0.0f;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) x[j] += one[e][j] * f;
+    }
   }
   const float g = sum > 0.0f ? 1.0f / sum : 0.0f;
   uint16_t *orow = a.o + (int64_t)qrow * a.os + (int64_t)h * kHd;
@@ -456,28 +496,55 @@ hipError_t launch(const AttnArgs &a, const AttnPlan &plan, hipStream_t stream) {
 
 }  // namespace
 
+// Both kernels' times are estimated from the average sequence and the smaller wins.  A
+// compute unit holds one workgroup of either, which costs a fixed time and one for each
+// 64 (128) keys it walks; the constants, in us, are fitted to 47 shapes of 1 to 64
+// sequences, 8 to 4096 queries and up to 16384 earlier keys.  Examples (many / few
+// queries' kernel, 16 and 8 heads of 128): 64 x 8 queries over 2056 keys 266 / 124 us;
+// 16 x 64 over 2112 67 / 61; 8 x 512 over 512 34 / 66; 1 x 4096 over 4096 113 / 229;
+// 1 x 512 over 16896 755 / 192.
 AttnPlan plan_attention(const puro_attention_shape &a) {
   AttnPlan p{};
-  p.splits = 1;
+  const double units = 256.0;
   const int64_t group = a.q_heads / a.k_heads;
-  p.fold = a.window > 0 ? 1 : 2;
-  const int64_t big = a.q_tokens / (kFwdRows * p.fold) + a.sequences;
   const int64_t few = a.q_tokens * group / kSplitRows + a.sequences;
-  p.split = big * a.q_heads < 128;
-  p.slots = (int)(p.split ? few : big);
-  if (p.split) {
-    // Enough workgroups for the 256 compute units twice over, but at least 8 chunks of
-    // keys for each.
-    int64_t keys = a.max_k > 0 ? a.max_k : a.k_tokens / a.sequences;
-    if (a.window > 0 && keys > a.window + a.sinks + 64) keys = a.window + a.sinks + 64;
-    int64_t splits = (512 + few * a.k_heads - 1) / (few * a.k_heads);
-    const int64_t most = keys / (8 * kSplitKeys);
-    if (splits > most) splits = most;
-    if (splits > 128) splits = 128;
-    if (splits < 1) splits = 1;
+  const double ql = (double)a.q_tokens / a.sequences;
+  double kl = a.max_k > 0 ? (double)a.max_k : (double)a.k_tokens / a.sequences;
+  const double far = a.window > 0 ? (double)(a.window + a.sinks) : kl;
+  // Keys that a tile of `rows` queries walks, at most and on average.
+  auto most = [&](double rows) {
+    const double see = far + (rows < ql ? rows : ql);
+    return kl < see ? kl : see;
+  };
+  auto mean = [&](double rows) {
+    const double all = kl > ql / 2 ? kl - ql / 2 : 0;
+    return all < most(rows) ? all : most(rows);
+  };
+
+  // Few queries' kernel: splits fill the units once, empty tiles counted (a 257th
+  // workgroup waits for a place: 16 x 16 queries over 2064 keys took 38 us split in two,
+  // 30 us whole), and hold at least 4 chunks of keys a wave.
+  const double wf = (double)a.sequences * (int64_t)((ql * group + kSplitRows - 1) / kSplitRows) * a.k_heads;
+  int64_t splits = 256 / (few * a.k_heads);
+  const int64_t longest = (int64_t)(most(1) / (4 * kSplitWaves * kSplitKeys));
+  if (splits > longest) splits = longest;
+  if (splits > kMostSplits) splits = kMostSplits;
+  if (splits < 1) splits = 1;
+  const double per_few = a.head_dim == 128 ? 1.5 : 0.6, per_many = a.head_dim == 128 ? 1.6 : 1.3;
+  const double walk_few = wf < units ? most(1) / splits : mean(1);
+  const double t_few = (wf < units ? 1 : wf / units) * (4 + per_few * walk_few / (kSplitWaves * kSplitKeys));
+  const double wm = (double)a.sequences * (int64_t)((ql + kFwdRows - 1) / kFwdRows) * a.q_heads;
+  const double t_many = (wm < units ? 1 : wm / units) * (5 + per_many * (wm < units ? most(kFwdRows) : mean(kFwdRows)) / kFwdKeys);
+
+  p.split = t_few < t_many;
+  p.splits = 1;
+  // Tiles in pairs, of equal work without a window, once every unit gets two of them
+  // (4 x 4096 tokens: 289 against 294 us one by one).
+  p.fold = a.window == 0 && wm >= 2 * units ? 2 : 1;
+  p.slots = (int)(p.split ? few : a.q_tokens / (kFwdRows * p.fold) + a.sequences);
+  if (p.split && splits > 1) {
     p.splits = (int)splits;
-    if (splits > 1)
-      p.ws_bytes = (size_t)few * (size_t)a.k_heads * (size_t)splits * (size_t)kSplitRows * (size_t)(a.head_dim + 2) * 4;
+    p.ws_bytes = (size_t)few * (size_t)a.k_heads * (size_t)splits * (size_t)kSplitRows * (size_t)(a.head_dim + 2) * 4;
   }
   return p;
 }
