@@ -58,27 +58,36 @@ for _name, _args, _res in (
 
 
 # ---------------------------------------------------------------- argument checks
+# The handle of a device's current stream, without the torch.cuda.Stream object that
+# torch.cuda.current_stream builds (3 us of a call whose kernel may take 3).
+_current = torch._C._cuda_getCurrentRawStream
+
+
+def _stream(stream, device):
+    return _current(device.index) if stream is None else getattr(stream, "cuda_stream", stream)
+
+
 def _heads_tensor(t, name, heads=None, head_dim=None, tokens=None, device=None):
     """A [tokens][heads][head_dim] bf16 CUDA tensor with packed heads; returns its token stride."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 3:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or not t.is_cuda or t.dim() != 3:
         raise TypeError("%s must be a bfloat16 CUDA tensor [tokens][heads][head_dim]" % name)
     n, h, d = t.shape
     if (heads is not None and h != heads) or (head_dim is not None and d != head_dim) or (tokens is not None and n != tokens):
         raise ValueError("%s must have shape %s, got %s" % (name, (tokens, heads, head_dim), tuple(t.shape)))
     if device is not None and t.device != device:
         raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
-    s = t.stride()
-    if (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
+    s, sh, sd = t.stride()
+    if (d > 1 and sd != 1) or (h > 1 and sh != d):
         raise ValueError("%s must have densely packed heads" % name)
-    return s[0] if n > 1 else -(-(max(s[0], h * d)) // 8) * 8
+    return s if n > 1 else -(-(max(s, h * d)) // 8) * 8
 
 
 def _ints(t, name, n, device):
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or not t.is_cuda:
         raise TypeError("%s must be an int32 CUDA tensor" % name)
-    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
         raise ValueError("%s must be contiguous with shape (%d,)" % (name, n))
     if t.device != device:
         raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
@@ -134,7 +143,7 @@ def rope_table(positions: int, rot: int, base: float = 10000.0, scaling: str = "
     table = _puro.empty((positions, 2, rot // 2), dtype=torch.float32, device=device)
     with torch.cuda.device(table.device):
         _puro._check(_lib.puro_rope_table(positions, rot, base, _SCALINGS[scaling], factor, trained, table.data_ptr(),
-                                          _puro._stream(stream)), "puro_rope_table")
+                                          _stream(stream, table.device)), "puro_rope_table")
     return table
 
 
@@ -146,7 +155,7 @@ def rope(x, table, pos=None, layout: str = "half", inverse: bool = False, out=No
     n, h, d = x.shape
     r = _rotation(table, pos, layout, n, d, x.device)
     y, ys = _out(out, "out", (n, h, d), x.device)
-    _puro._check(_lib.puro_rope(r, inverse, x.data_ptr(), xs, n, h, d, y.data_ptr(), ys, _puro._stream(stream)), "puro_rope")
+    _puro._check(_lib.puro_rope(r, inverse, x.data_ptr(), xs, n, h, d, y.data_ptr(), ys, _stream(stream, x.device)), "puro_rope")
     return y
 
 
@@ -164,7 +173,7 @@ def qk_norm_rope(x, wq, wk, table, pos=None, *, q_heads: int, k_heads: int, eps:
     q, qs = _out(q, "q", (n, q_heads, d), dev)
     k, ks = _out(k, "k", (n, k_heads, d), dev)
     _puro._check(_lib.puro_qk_norm_rope(r, x.data_ptr(), xs, n, q_heads, k_heads, d, pq, pk, eps, q.data_ptr(), qs,
-                                        k.data_ptr(), ks, _puro._stream(stream)), "puro_qk_norm_rope")
+                                        k.data_ptr(), ks, _stream(stream, dev)), "puro_qk_norm_rope")
     return q, k
 
 
@@ -185,7 +194,7 @@ def qk_norm_rope_append(x, wq, wk, table, pos, cache_k, cache_v, rows, *, q_head
     q, qs = _out(q, "q", (n, q_heads, d), dev)
     _puro._check(_lib.puro_qk_norm_rope_append(r, x.data_ptr(), xs, n, q_heads, kh, d, pq, pk, eps, q.data_ptr(), qs,
                                                cache_k.data_ptr(), ks, cache_v.data_ptr(), vs, pr, cache_k.shape[0],
-                                               _puro._stream(stream)), "puro_qk_norm_rope_append")
+                                               _stream(stream, dev)), "puro_qk_norm_rope_append")
     return q
 
 
@@ -209,7 +218,7 @@ def qk_norm_rope_backward(dq, dk, x, wq, wk, table, pos=None, *, eps: float = 1e
     workspace, size = _workspace(workspace, _lib.puro_qk_norm_rope_backward_workspace_bytes(n, d), dev)
     _puro._check(_lib.puro_qk_norm_rope_backward(r, dq.data_ptr(), dqs, dk.data_ptr(), dks, x.data_ptr(), xs, n, qh, kh,
                                                  d, pq, pk, eps, dx.data_ptr(), dxs, dw.data_ptr(),
-                                                 dw.data_ptr() + 4 * d, workspace, size, _puro._stream(stream)),
+                                                 dw.data_ptr() + 4 * d, workspace, size, _stream(stream, dev)),
                  "puro_qk_norm_rope_backward")
     return dx, dw[0], dw[1]
 
@@ -263,7 +272,7 @@ def attention(q, k, v, q_start=None, k_start=None, k_len=None, *, window: int = 
     lse = _puro.empty((a.q_heads, a.q_tokens), dtype=torch.float32, device=q.device)
     ws, size = _workspace(workspace, _lib.puro_attention_workspace_bytes(a), q.device)
     _puro._check(_lib.puro_attention(a, q.data_ptr(), k.data_ptr(), v.data_ptr(), pqs, pks, pkl, o.data_ptr(),
-                                     lse.data_ptr(), ws, size, _puro._stream(stream)), "puro_attention")
+                                     lse.data_ptr(), ws, size, _stream(stream, q.device)), "puro_attention")
     return o, lse
 
 
@@ -285,5 +294,5 @@ def attention_backward(do, q, k, v, o, lse, q_start=None, k_start=None, *, windo
     ws, size = _workspace(workspace, _lib.puro_attention_backward_workspace_bytes(a), dev)
     _puro._check(_lib.puro_attention_backward(a, do.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                                               lse.data_ptr(), pqs, pks, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws,
-                                              size, _puro._stream(stream)), "puro_attention_backward")
+                                              size, _stream(stream, dev)), "puro_attention_backward")
     return dq, dk, dv
