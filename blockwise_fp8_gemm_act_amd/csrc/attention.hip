@@ -80,7 +80,7 @@ __device__ __forceinline__ void meet() {
 __device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 template <int kHd>
-__global__ void __launch_bounds__(64 * kFwdWaves, 2) attn_kernel(AttnArgs a, int slots, int fold) {
+__global__ void __launch_bounds__(64 * kFwdWaves, 2) attn_kernel(AttnArgs a, int slots) {
   constexpr int kTile = kTileBytes<kHd>(kFwdKeys);
   __shared__ __attribute__((aligned(1024))) uint8_t lds[6 * kTile];     // three places of keys, three of values
   const int lane = threadIdx.x & 63, half = lane >> 5;
@@ -91,158 +91,152 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 2) attn_kernel(AttnArgs a, int
   const int hk = (int)(blockIdx.x % a.k_heads);
   const int rest = (int)(blockIdx.x / a.k_heads);
   const int h = hk * a.group + rest % a.group;
-  int slot = slots - 1 - rest / a.group;
-  const Seq sq = load_seq(a, find_seq(a.q_start, a.sequences, a.q_tokens, 1, kFwdRows * fold, slot));
-  const int tiles = (int)(((int64_t)sq.ql + kFwdRows - 1) / kFwdRows);
-  if ((int64_t)slot * fold >= tiles) return;
+  int slot = slots - 1 - Order(slots, a.sequences, a.window)(rest / a.group);
+  if (slot < 0) return;
+  const Seq sq = load_seq(a, find_seq(a.q_start, a.sequences, a.q_tokens, 1, kFwdRows, slot));
+  if ((int64_t)slot * kFwdRows >= sq.ql) return;
   const int shift = sq.kl - sq.ql;                              // position of query 0
   const TileCopy<kHd> keys(a.k + (int64_t)sq.k0 * a.ks + (int64_t)hk * kHd, a.ks);
   const TileCopy<kHd> vals(a.v + (int64_t)sq.k0 * a.vs + (int64_t)hk * kHd, a.vs);
   const uint32_t lds0 = lds_addr(lds);
   const float c2 = a.scale * kLog2e;
 
-  // With fold 2 a workgroup takes a sequence's tile from its end and the one as far
-  // from its start: together they see the same number of keys everywhere.
-  for (int turn = 0; turn < fold; ++turn) {
-    const int tile = turn == 0 && fold == 2 ? tiles - 1 - slot : slot;
-    if (turn == 1 && tile == tiles - 1 - slot) break;
-    const int row0 = tile * kFwdRows;
-    const int rows = sq.ql - row0 < kFwdRows ? sq.ql - row0 : kFwdRows;
-    const KeyTiles kt = key_tiles(shift + row0, shift + row0 + rows - 1, a.window, a.sinks, kFwdKeys);
-    const int mine = 32 * wave + (lane & 31);                     // this lane's query in the block
-    const int qrow = sq.q0 + row0 + (mine < rows ? mine : rows - 1);
-    const int p = shift + row0 + mine;
-    const int w_lo = shift + row0 + 32 * wave, w_hi = w_lo + 31;  // positions of the wave's queries
-    // Tiles past the wave's last query are only copied for the others.
-    int seen = kt.count;
-    while (seen > 0 && kt.key0(seen - 1, kFwdKeys) > w_hi) --seen;
-    bf16x8 qf[kHd / 16];
+  const int row0 = slot * kFwdRows;
+  const int rows = sq.ql - row0 < kFwdRows ? sq.ql - row0 : kFwdRows;
+  const KeyTiles kt = key_tiles(shift + row0, shift + row0 + rows - 1, a.window, a.sinks, kFwdKeys);
+  const int mine = 32 * wave + (lane & 31);                     // this lane's query in the block
+  const int qrow = sq.q0 + row0 + (mine < rows ? mine : rows - 1);
+  const int p = shift + row0 + mine;
+  const int w_lo = shift + row0 + 32 * wave, w_hi = w_lo + 31;  // positions of the wave's queries
+  // Tiles past the wave's last query are only copied for the others.
+  int seen = kt.count;
+  while (seen > 0 && kt.key0(seen - 1, kFwdKeys) > w_hi) --seen;
+  bf16x8 qf[kHd / 16];
 #pragma unroll
-    for (int kk = 0; kk < kHd / 16; ++kk)
-      qf[kk] = load8(a.q + (int64_t)qrow * a.qs + (int64_t)h * kHd + 16 * kk + 8 * half);
+  for (int kk = 0; kk < kHd / 16; ++kk)
+    qf[kk] = load8(a.q + (int64_t)qrow * a.qs + (int64_t)h * kHd + 16 * kk + 8 * half);
 
-    // Opaque, so that a read's address stays one register plus a constant.
-    auto place = [&](int n) {
-      uint32_t at = lds0 + (uint32_t)(n * kTile);
-      asm("" : "+s"(at));
-      return at;
-    };
-    auto key_place = [&](int i) { return place(i % 3); };
-    auto value_place = [&](int i) { return place(3 + i % 3); };
-    // This wave's part of a tile's copies, in kParts groups.  Past the last tile that one
-    // is copied again, to a place that is not read any more.
-    constexpr int kParts = kFwdKeys / kGroupRows<kHd> / kFwdWaves;
-    auto copy_keys = [&](int i, int part) {
-      keys(kt, i < kt.count ? i : kt.count - 1, kFwdKeys, part * kFwdWaves + wave, key_place(i));
-    };
-    auto copy_values = [&](int i, int part) {
-      vals(kt, i < kt.count ? i : kt.count - 1, kFwdKeys, part * kFwdWaves + wave, value_place(i));
-    };
+  // Opaque, so that a read's address stays one register plus a constant.
+  auto place = [&](int n) {
+    uint32_t at = lds0 + (uint32_t)(n * kTile);
+    asm("" : "+s"(at));
+    return at;
+  };
+  auto key_place = [&](int i) { return place(i % 3); };
+  auto value_place = [&](int i) { return place(3 + i % 3); };
+  // This wave's part of a tile's copies, in kParts groups.  Past the last tile that one
+  // is copied again, to a place that is not read any more.
+  constexpr int kParts = kFwdKeys / kGroupRows<kHd> / kFwdWaves;
+  auto copy_keys = [&](int i, int part) {
+    keys(kt, i < kt.count ? i : kt.count - 1, kFwdKeys, part * kFwdWaves + wave, key_place(i));
+  };
+  auto copy_values = [&](int i, int part) {
+    vals(kt, i < kt.count ? i : kt.count - 1, kFwdKeys, part * kFwdWaves + wave, value_place(i));
+  };
 
-    Row<kHd> st;
-    st.clear();
-    f32x16 s[2];
-    bf16x8 pf[2][2];
-    auto score = [&](int i, int b) { s[b] = score_tile<kHd>(key_place(i), 32 * b, qf); };
-    auto values = [&](int i, int b) {
-      const uint32_t vtile = value_place(i);
+  Row<kHd> st;
+  st.clear();
+  f32x16 s[2];
+  bf16x8 pf[2][2];
+  auto score = [&](int i, int b) { s[b] = score_tile<kHd>(key_place(i), 32 * b, qf); };
+  auto values = [&](int i, int b) {
+    const uint32_t vtile = value_place(i);
 #pragma unroll
-      for (int step = 0; step < 2; ++step)
+    for (int step = 0; step < 2; ++step)
 #pragma unroll
-        for (int d = 0; d < kHd / 32; ++d)
-          st.o[d] = mfma(col_frag<kHd>(vtile, 32 * b + 16 * step, d), pf[b][step], st.o[d]);
-    };
-    // exp2 of 32 keys' scores, their sum, and the packed probabilities.
-    auto exps = [&](f32x16 x, int b) {
-      float sum[2] = {0.0f, 0.0f};
+      for (int d = 0; d < kHd / 32; ++d)
+        st.o[d] = mfma(col_frag<kHd>(vtile, 32 * b + 16 * step, d), pf[b][step], st.o[d]);
+  };
+  // exp2 of 32 keys' scores, their sum, and the packed probabilities.
+  auto exps = [&](f32x16 x, int b) {
+    float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        x[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], c2, -st.m));
-        sum[j & 1] += x[j];
-      }
-      st.l += sum[0] + sum[1];
-      pf[b][0] = pack_step(x, 0);
-      pf[b][1] = pack_step(x, 1);
-    };
-    // Mask, maximum and exponentials of tile i.  (Moving exponentials between the
-    // products, one half or all of them, made those turns longer by more: 344 to 426 us
-    // against 289 at 4 x 4096 tokens, 16 and 8 heads of 128.)
-    auto softmax = [&](int i) {
-      const int key0 = kt.key0(i, kFwdKeys);
-      const bool all = key0 + kFwdKeys - 1 <= w_lo && (a.window == 0 || key0 > w_hi - a.window);
-      if (!all) {
-        mask_tile(s[0], key0, p, a.window, a.sinks);
-        mask_tile(s[1], key0 + 32, p, a.window, a.sinks);
-      }
-      st.raise(half_max(fmaxf(tile_max(s[0]), tile_max(s[1]))) * c2);
-      exps(s[0], 0);
-      exps(s[1], 1);
-    };
-
-    arrived(qf);
-    if (kt.count > 0) {
-#pragma unroll
-      for (int part = 0; part < kParts; ++part) {
-        copy_keys(0, part);
-        copy_values(0, part);
-        copy_keys(1, part);
-        copy_values(1, part);
-        copy_keys(2, part);
-      }
+    for (int j = 0; j < 16; ++j) {
+      x[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], c2, -st.m));
+      sum[j & 1] += x[j];
     }
+    st.l += sum[0] + sum[1];
+    pf[b][0] = pack_step(x, 0);
+    pf[b][1] = pack_step(x, 1);
+  };
+  // Mask, maximum and exponentials of tile i.  (Moving exponentials between the
+  // products, one half or all of them, made those turns longer by more: 344 to 426 us
+  // against 289 at 4 x 4096 tokens, 16 and 8 heads of 128.)
+  auto softmax = [&](int i) {
+    const int key0 = kt.key0(i, kFwdKeys);
+    const bool all = key0 + kFwdKeys - 1 <= w_lo && (a.window == 0 || key0 > w_hi - a.window);
+    if (!all) {
+      mask_tile(s[0], key0, p, a.window, a.sinks);
+      mask_tile(s[1], key0 + 32, p, a.window, a.sinks);
+    }
+    st.raise(half_max(fmaxf(tile_max(s[0]), tile_max(s[1]))) * c2);
+    exps(s[0], 0);
+    exps(s[1], 1);
+  };
+
+  arrived(qf);
+  if (kt.count > 0) {
+#pragma unroll
+    for (int part = 0; part < kParts; ++part) {
+      copy_keys(0, part);
+      copy_values(0, part);
+      copy_keys(1, part);
+      copy_values(1, part);
+      copy_keys(2, part);
+    }
+  }
+  landed();
+  meet();
+  if (seen > 0) {
+    score(0, 0);
+    score(0, 1);
+    if (!late) softmax(0);
+  }
+  meet();
+  if (late) {
+    if (seen > 0) softmax(0);
+    meet();
+  }
+  int i = 0;
+  for (; i + 1 < seen; ++i) {
+    score(i + 1, 0);
+    copy_keys(i + 3, 0);
+    score(i + 1, 1);
+    copy_values(i + 2, 0);
+    values(i, 0);
+    if (kParts > 1) copy_keys(i + 3, kParts - 1);
+    values(i, 1);
+    if (kParts > 1) copy_values(i + 2, kParts - 1);
+    feed<4, kHd / 8, kHd / 8>();
+    meet();
+    softmax(i + 1);
     landed();
     meet();
-    if (seen > 0) {
-      score(0, 0);
-      score(0, 1);
-      if (!late) softmax(0);
+  }
+  for (; i < kt.count; ++i) {
+    if (i + 1 == seen) {
+        values(i, 0);
+      values(i, 1);
+    }
+#pragma unroll
+    for (int part = 0; part < kParts; ++part) {
+      copy_keys(i + 3, part);
+      copy_values(i + 2, part);
     }
     meet();
-    if (late) {
-      if (seen > 0) softmax(0);
-      meet();
-    }
-    int i = 0;
-    for (; i + 1 < seen; ++i) {
-      score(i + 1, 0);
-      copy_keys(i + 3, 0);
-      score(i + 1, 1);
-      copy_values(i + 2, 0);
-      values(i, 0);
-      if (kParts > 1) copy_keys(i + 3, kParts - 1);
-      values(i, 1);
-      if (kParts > 1) copy_values(i + 2, kParts - 1);
-      feed<4, kHd / 8, kHd / 8>();
-      meet();
-      softmax(i + 1);
-      landed();
-      meet();
-    }
-    for (; i < kt.count; ++i) {
-      if (i + 1 == seen) {
-          values(i, 0);
-        values(i, 1);
-      }
-#pragma unroll
-      for (int part = 0; part < kParts; ++part) {
-        copy_keys(i + 3, part);
-        copy_values(i + 2, part);
-      }
-      meet();
-      landed();
-      meet();
-    }
-    if (!late) meet();
+    landed();
+    meet();
+  }
+  if (!late) meet();
 
-    const float l = half_sum(st.l);
-    if (mine < rows) {
-      const float f = l > 0.0f ? 1.0f / l : 0.0f;
-      uint16_t *orow = a.o + (int64_t)qrow * a.os + (int64_t)h * kHd;
+  const float l = half_sum(st.l);
+  if (mine < rows) {
+    const float f = l > 0.0f ? 1.0f / l : 0.0f;
+    uint16_t *orow = a.o + (int64_t)qrow * a.os + (int64_t)h * kHd;
 #pragma unroll
-      for (int d = 0; d < kHd / 32; ++d) store_block(orow + 32 * d, st.o[d], f);
-      if (a.lse && half == 0)
-        a.lse[(int64_t)h * a.q_tokens + qrow] = l > 0.0f ? (st.m + __builtin_log2f(l)) * kLn2 : -__builtin_inff();
-    }
+    for (int d = 0; d < kHd / 32; ++d) store_block(orow + 32 * d, st.o[d], f);
+    if (a.lse && half == 0)
+      a.lse[(int64_t)h * a.q_tokens + qrow] = l > 0.0f ? (st.m + __builtin_log2f(l)) * kLn2 : -__builtin_inff();
   }
 }
 
@@ -480,7 +474,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int splits) 
 template <int kHd>
 hipError_t launch(const AttnArgs &a, const AttnPlan &plan, hipStream_t stream) {
   if (!plan.split) {
-    attn_kernel<kHd><<<dim3((unsigned)((int64_t)plan.slots * a.q_heads)), dim3(64 * kFwdWaves), 0, stream>>>(a, plan.slots, plan.fold);
+    attn_kernel<kHd><<<dim3((unsigned)((int64_t)Order(plan.slots, a.sequences, a.window).count() * a.q_heads)), dim3(64 * kFwdWaves), 0, stream>>>(a, plan.slots);
     return hipGetLastError();
   }
   attn_split_kernel<kHd><<<dim3((unsigned)((int64_t)plan.slots * a.k_heads * plan.splits)), dim3(64 * kSplitWaves), 0,
@@ -538,10 +532,7 @@ AttnPlan plan_attention(const puro_attention_shape &a) {
 
   p.split = t_few < t_many;
   p.splits = 1;
-  // Tiles in pairs, of equal work without a window, once every unit gets two of them
-  // (4 x 4096 tokens: 289 against 294 us one by one).
-  p.fold = a.window == 0 && wm >= 2 * units ? 2 : 1;
-  p.slots = (int)(p.split ? few : a.q_tokens / (kFwdRows * p.fold) + a.sequences);
+  p.slots = (int)(p.split ? few : a.q_tokens / kFwdRows + a.sequences);
   if (p.split && splits > 1) {
     p.splits = (int)splits;
     p.ws_bytes = (size_t)few * (size_t)a.k_heads * (size_t)splits * (size_t)kSplitRows * (size_t)(a.head_dim + 2) * 4;

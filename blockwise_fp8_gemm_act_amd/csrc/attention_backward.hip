@@ -28,7 +28,8 @@ __global__ void __launch_bounds__(64 * kDqWaves, 2) attn_dq_kernel(AttnArgs a, i
   const int hk = (int)(blockIdx.x % a.k_heads);
   const int rest = (int)(blockIdx.x / a.k_heads);
   const int h = hk * a.group + rest % a.group;
-  int slot = slots - 1 - rest / a.group;
+  int slot = slots - 1 - Order(slots, a.sequences, a.window)(rest / a.group);
+  if (slot < 0) return;
   const Seq sq = load_seq(a, find_seq(a.q_start, a.sequences, a.q_tokens, 1, kDqRows, slot));
   if ((int64_t)slot * kDqRows >= sq.ql) return;
   const int row0 = slot * kDqRows;
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
   int rest = (int)(blockIdx.x / a.k_heads);
   const int far_items = plan.far_slots * plan.far_blocks;
   const bool far = rest < far_items;
-  int part, parts, slot, s;
+  int part, parts, slot, s, number = 0;
   if (far) {
     slot = rest % plan.far_blocks;
     part = rest / plan.far_blocks;
@@ -203,7 +204,8 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
     rest -= far_items;
     part = rest % plan.parts;
     parts = plan.parts;
-    slot = rest / plan.parts;
+    slot = Order(plan.slots, a.sequences, a.window)(rest / plan.parts);
+    number = slot;
     s = find_seq(a.k_start, a.sequences, a.k_tokens, 1, kDkRows, slot);
   }
   const Seq sq = load_seq(a, s);
@@ -215,7 +217,7 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
     parts = fars;
     partial = a.ws + plan.far_at + (size_t)(blockIdx.x) * part_floats<kHd>();
   } else if (parts > 1) {
-    partial = a.ws + plan.near_at + ((size_t)(rest / parts * a.k_heads + hk) * parts + part) * part_floats<kHd>();
+    partial = a.ws + plan.near_at + ((size_t)(number * a.k_heads + hk) * parts + part) * part_floats<kHd>();
   } else if (fars > 0) {
     partial = a.ws + plan.edge_at + (size_t)((s * plan.far_blocks + slot) * a.k_heads + hk) * part_floats<kHd>();
   }
@@ -426,12 +428,12 @@ template <int kHd>
 hipError_t launch(const AttnArgs &a, hipStream_t stream) {
   if (a.q_tokens > 0) {
     const int slots = a.q_tokens / kDqRows + a.sequences;
-    attn_dq_kernel<kHd><<<dim3((unsigned)((int64_t)slots * a.q_heads)), dim3(64 * kDqWaves), 0, stream>>>(a, slots);
+    attn_dq_kernel<kHd><<<dim3((unsigned)((int64_t)Order(slots, a.sequences, a.window).count() * a.q_heads)), dim3(64 * kDqWaves), 0, stream>>>(a, slots);
     if (hipError_t e = hipGetLastError()) return e;
   }
   if (a.k_tokens == 0) return hipSuccess;
   const DkPlan plan = plan_dk(a.q_tokens, a.k_tokens, a.sequences, a.q_heads, a.k_heads, kHd, a.window, a.sinks);
-  const int64_t items = (int64_t)plan.far_slots * plan.far_blocks + (int64_t)plan.slots * plan.parts;
+  const int64_t items = (int64_t)plan.far_slots * plan.far_blocks + (int64_t)Order(plan.slots, a.sequences, a.window).count() * plan.parts;
   attn_dkdv_kernel<kHd><<<dim3((unsigned)(items * a.k_heads)), dim3(64 * kDkWaves), 0, stream>>>(a, plan);
   if (hipError_t e = hipGetLastError()) return e;
   if (plan.parts > 1 || plan.far_blocks > 0) {

@@ -98,6 +98,20 @@ __device__ __forceinline__ int find_seq(const int32_t *start, int sequences, int
   return s;
 }
 
+// Order in which tiles start.  Without a window a tile's work grows along its sequence:
+// the x-th numbers of `sequences` equal parts of the number line come before the next of
+// any, so that (with sequences alike) those that walk far start first in all of them and
+// the short ones fill the end.  A permutation in any case, up to numbers past the end,
+// which are no tiles.  4 x 4096 tokens backward: 1094 -> 975 us.  With a window the work
+// is even, and neighbours in the sequence share keys: as numbered.
+struct Order {
+  int slots, parts;
+  __device__ __host__ __forceinline__ Order(int slots, int sequences, int window) : slots(slots), parts(window > 0 ? 1 : sequences) {}
+  __device__ __host__ __forceinline__ int each() const { return (slots + parts - 1) / parts; }
+  __device__ __host__ __forceinline__ int count() const { return each() * parts; }
+  __device__ __forceinline__ int operator()(int x) const { return x % parts * each() + x / parts; }
+};
+
 // ---------------------------------------------------------------- mask
 // The key tiles that a block of queries at positions p_lo .. p_hi looks at, `unit`
 // keys each: those of the visible first keys, then those of the window.  Keys that

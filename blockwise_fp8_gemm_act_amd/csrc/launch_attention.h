@@ -74,7 +74,6 @@ struct AttnArgs {
 struct AttnPlan {
   bool split;        // the kernel for few queries: 32 (query, head) rows a tile, keys over waves and splits
   int slots;         // query tiles, empty ones included
-  int fold;          // query tiles of a workgroup (1 or 2) of the kernel for many queries
   int splits;        // key ranges of a tile
   size_t ws_bytes;   // fp32 partials, when splits > 1
 };
