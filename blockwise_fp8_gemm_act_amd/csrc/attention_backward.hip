@@ -249,9 +249,14 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
   const uint32_t lds0 = lds_addr(lds), stat0 = lds_addr(stat);
   int copy_r, copy_c;
   copy_place<kHd>(copy_r, copy_c);
-  auto copy = [&](int i, int buf) {
-    const int h = hk * a.group + i / tiles;
-    const int q0 = (tile0 + i % tiles) * kDkQueries;
+  // Tiles are walked head by head; the next one to copy:
+  int next_h = hk * a.group + (tiles > 0 ? begin / tiles : 0), next_t = tiles > 0 ? begin % tiles : 0;
+  auto copy = [&](int buf) {
+    const int h = next_h, q0 = (tile0 + next_t) * kDkQueries;
+    if (++next_t == tiles) {
+      next_t = 0;
+      ++next_h;
+    }
     const uint32_t at = lds0 + (uint32_t)(buf * 2 * kTile);
     const int last = sq.ql - 1 - q0;                     // rows past the sequence's end: its last one
     const uint16_t *qb = a.q + (int64_t)(sq.q0 + q0) * a.qs + (int64_t)h * kHd;
@@ -274,12 +279,14 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
 #pragma unroll
   for (int d = 0; d < kHd / 32; ++d) dk[d] = dv[d] = (f32x16){};
   const float c2 = a.scale * kLog2e;
-  if (begin < end) copy(begin, 0);
+  int now_t = next_t;
+  if (begin < end) copy(0);
   for (int i = begin; i < end; ++i) {
     const int buf = (i - begin) & 1;
     wait_all_and_meet();
-    if (i + 1 < end) copy(i + 1, buf ^ 1);
-    const int q0 = (tile0 + i % tiles) * kDkQueries;
+    const int q0 = (tile0 + now_t) * kDkQueries;
+    now_t = next_t;
+    if (i + 1 < end) copy(buf ^ 1);
     const uint32_t qtile = lds0 + (uint32_t)(buf * 2 * kTile), dtile = qtile + kTile;
 #pragma unroll 1
     for (int b = 0; b < 2; ++b) {
