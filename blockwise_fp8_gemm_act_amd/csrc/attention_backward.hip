@@ -55,11 +55,6 @@ __global__ void __launch_bounds__(64 * kDqWaves, 2) attn_dq_kernel(AttnArgs a, i
   dd = half_sum(dd);
   float lse2 = a.lse[(int64_t)h * a.q_tokens + qrow] * kLog2e;
   if (lse2 == -__builtin_inff()) lse2 = __builtin_inff();
-  if (half == 0 && mine < rows) {
-    a.ws[(int64_t)h * a.q_tokens + qrow] = lse2;
-    a.ws[(int64_t)(a.q_heads + h) * a.q_tokens + qrow] = dd;
-  }
-
   const TileCopy<kHd> keys(a.k + (int64_t)sq.k0 * a.ks + (int64_t)hk * kHd, a.ks);
   const TileCopy<kHd> vals(a.v + (int64_t)sq.k0 * a.vs + (int64_t)hk * kHd, a.vs);
   const uint32_t lds0 = lds_addr(lds);
@@ -74,10 +69,42 @@ __global__ void __launch_bounds__(64 * kDqWaves, 2) attn_dq_kernel(AttnArgs a, i
 
   arrived(qf);
   arrived(df);
+  const float c2 = a.scale * kLog2e;
+
+  // D = do.o carries the rounding of o to bf16.  Over n visible keys that is a 1/sqrt(n)
+  // part of dS's own rounding, but where a row sees a handful of keys it is all there is:
+  // with one key dS is 0.  Blocks with such rows first correct D by the sum of their dS,
+  // which is 0 for the exact D.
+  if (kt.count > 0 && (shift + row0 < 64 || (a.window > 0 && a.window + a.sinks < 64))) {
+    float off = 0.0f;
+    copy(0, 0);
+    for (int i = 0; i < kt.count; ++i) {
+      wait_all_and_meet();
+      if (i + 1 < kt.count) copy(i + 1, (i + 1) & 1);
+      const uint32_t ktile = lds0 + (uint32_t)((i & 1) * 2 * kTile), vtile = ktile + kTile;
+#pragma unroll 1
+      for (int b = 0; b < 2; ++b) {
+        f32x16 s = {}, dp = {};
+#pragma unroll
+        for (int kk = 0; kk < kHd / 16; ++kk) s = mfma(row_frag<kHd>(ktile, 32 * b, kk), qf[kk], s);
+#pragma unroll
+        for (int kk = 0; kk < kHd / 16; ++kk) dp = mfma(row_frag<kHd>(vtile, 32 * b, kk), df[kk], dp);
+        mask_tile(s, kt.key0(i, kDqKeys) + 32 * b, p, a.window, a.sinks);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) off += __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], c2, -lse2)) * (dp[j] - dd);
+      }
+    }
+    dd += half_sum(off);
+    wait_all_and_meet();
+  }
+  if (half == 0 && mine < rows) {
+    a.ws[(int64_t)h * a.q_tokens + qrow] = lse2;
+    a.ws[(int64_t)(a.q_heads + h) * a.q_tokens + qrow] = dd;
+  }
+
   f32x16 acc[kHd / 32];
 #pragma unroll
   for (int d = 0; d < kHd / 32; ++d) acc[d] = (f32x16){};
-  const float c2 = a.scale * kLog2e;
   if (kt.count > 0) copy(0, 0);
   for (int i = 0; i < kt.count; ++i) {
     wait_all_and_meet();
