@@ -140,11 +140,10 @@ __device__ __forceinline__ KeyTiles key_tiles(int p_lo, int p_hi, int window, in
 // A tile holds rows of kHd bf16 in groups of 1 KB (4 rows of 128 columns, or 8 of
 // 64), each one copy of a wave, 16 bytes between groups.  Inside a group 4 rows by 64
 // bytes are contiguous: chunk c (16 bytes) of row r of 4 lies at 256 (c/4) + 64 r + 16
-// (c%4); with 64 columns the second 4 rows follow at 512 with the halves of their 64
-// bytes swapped.  Then
-//   - a row fragment (16 rows, one chunk, per phase) touches all 64 banks once, or
-//     nearly: the 4 rows of a block lie 64 bytes apart, the blocks 16 or 32;
-//   - a transposed fragment (4 rows by 64 bytes) is 256 contiguous bytes;
+// (c%4); with 64 columns the second 4 rows follow at 512.  Then
+//   - a row fragment's phase (16 rows, one chunk) and a transposed fragment's (4 rows
+//     by 64 bytes, contiguous) spread over the 64 banks: the hardware counts no
+//     conflicts;
 //   - every address is one lane-dependent base plus a constant, so that the reads
 //     cost no address arithmetic (an xor swizzle took 24 registers or as many
 //     instructions a tile).
@@ -198,7 +197,7 @@ __device__ __forceinline__ void copy_place(int &r, int &c) {
     c = 4 * (lane >> 4) + (lane & 3);
   } else {
     r = ((lane >> 2) & 3) + 4 * (lane >> 5);
-    c = 4 * ((lane >> 4) & 1) + ((lane & 3) ^ (2 * (lane >> 5)));
+    c = 4 * ((lane >> 4) & 1) + (lane & 3);
   }
 }
 
@@ -245,13 +244,8 @@ __device__ __forceinline__ bf16x8 row_frag(uint32_t tile, int r0, int kk) {
   const int lane = threadIdx.x & 63;
   const int r = lane & 31;
   uint32_t base = (uint32_t)(r / kGroupRows<kHd> * kGroupBytes + (r & 3) * 64 + (lane >> 5) * 16);
-  uint32_t step = (uint32_t)((kk & 1) * 32);
-  if (kHd == 64) {
-    const uint32_t swap = (uint32_t)((r >> 2) & 1);
-    base += swap * 512;
-    step = (kk & 1) ? 32 - 32 * swap : 32 * swap;
-  }
-  return *(lds_bf16x8 *)(uintptr_t)(tile + base + step + (uint32_t)((kk >> 1) * 256 + kTileBytes<kHd>(r0)));
+  if (kHd == 64) base += (uint32_t)(((r >> 2) & 1) * 512);
+  return *(lds_bf16x8 *)(uintptr_t)(tile + base + (uint32_t)((kk >> 1) * 256 + (kk & 1) * 32 + kTileBytes<kHd>(r0)));
 }
 
 // The transpose's fragment: lane l gets column 32 db + (l & 31) of the 8 rows r0 +
@@ -261,11 +255,7 @@ template <int kHd>
 __device__ __forceinline__ bf16x8 col_frag(uint32_t tile, int r0, int db) {
   const int lane = threadIdx.x & 63;
   const int half = lane >> 5, i = lane & 15;
-  uint32_t base = (uint32_t)((i >> 2) * 64 + (i & 3) * 8);
-  if (kHd == 128)
-    base += (uint32_t)(half * kGroupBytes + (lane & 16) * 2);
-  else
-    base += (uint32_t)(half * 512 + ((lane & 16) * 2 ^ half * 32));
+  const uint32_t base = (uint32_t)((i >> 2) * 64 + (i & 3) * 8 + (lane & 16) * 2 + half * (kHd == 128 ? kGroupBytes : 512));
   bf16x4 v[2];
 #pragma unroll
   for (int w = 0; w < 2; ++w)
