@@ -56,7 +56,9 @@ __device__ __forceinline__ float tile_max(const f32x16 &s) {
 }
 
 // ---------------------------------------------------------------- many queries
-constexpr int kFwdWaves = 8, kFwdRows = 32 * kFwdWaves, kFwdKeys = 64;
+constexpr int kFwdWaves = 8, kFwdKeys = 64;
+// (query, head) rows of a workgroup; `pack` heads of a group by kFwdRows / pack queries.
+constexpr int kFwdRows = 32 * kFwdWaves;
 
 // The two waves of a SIMD take turns: while one multiplies (scores of the next tile,
 // values of this one), the other does the softmax of its next tile, with a barrier
@@ -80,7 +82,7 @@ __device__ __forceinline__ void meet() {
 __device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 template <int kHd>
-__global__ void __launch_bounds__(64 * kFwdWaves, 2) attn_kernel(AttnArgs a, int slots) {
+__global__ void __launch_bounds__(64 * kFwdWaves, 2) attn_kernel(AttnArgs a, int slots, int pack) {
   constexpr int kTile = kTileBytes<kHd>(kFwdKeys);
   __shared__ __attribute__((aligned(1024))) uint8_t lds[6 * kTile];     // three places of keys, three of values
   const int lane = threadIdx.x & 63, half = lane >> 5;
@@ -90,24 +92,25 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 2) attn_kernel(AttnArgs a, int
   // serves one; the last tiles of a sequence, which see most keys, start first.
   const int hk = (int)(blockIdx.x % a.k_heads);
   const int rest = (int)(blockIdx.x / a.k_heads);
-  const int h = hk * a.group + rest % a.group;
-  int slot = slots - 1 - Order(slots, a.sequences, a.window)(rest / a.group);
+  const int packs = a.group / pack, tall = kFwdRows / pack;     // head packs of a group; queries of a block
+  const int h = hk * a.group + rest % packs * pack + wave * 32 / tall;
+  int slot = slots - 1 - Order(slots, a.sequences, a.window)(rest / packs);
   if (slot < 0) return;
-  const Seq sq = load_seq(a, find_seq(a.q_start, a.sequences, a.q_tokens, 1, kFwdRows, slot));
-  if ((int64_t)slot * kFwdRows >= sq.ql) return;
+  const Seq sq = load_seq(a, find_seq(a.q_start, a.sequences, a.q_tokens, 1, tall, slot));
+  if ((int64_t)slot * tall >= sq.ql) return;
   const int shift = sq.kl - sq.ql;                              // position of query 0
   const TileCopy<kHd> keys(a.k + (int64_t)sq.k0 * a.ks + (int64_t)hk * kHd, a.ks);
   const TileCopy<kHd> vals(a.v + (int64_t)sq.k0 * a.vs + (int64_t)hk * kHd, a.vs);
   const uint32_t lds0 = lds_addr(lds);
   const float c2 = a.scale * kLog2e;
 
-  const int row0 = slot * kFwdRows;
-  const int rows = sq.ql - row0 < kFwdRows ? sq.ql - row0 : kFwdRows;
+  const int row0 = slot * tall;
+  const int rows = sq.ql - row0 < tall ? sq.ql - row0 : tall;
   const KeyTiles kt = key_tiles(shift + row0, shift + row0 + rows - 1, a.window, a.sinks, kFwdKeys);
-  const int mine = 32 * wave + (lane & 31);                     // this lane's query in the block
+  const int wave0 = wave * 32 % tall, mine = wave0 + (lane & 31);   // the wave's first query in the block, this lane's
   const int qrow = sq.q0 + row0 + (mine < rows ? mine : rows - 1);
   const int p = shift + row0 + mine;
-  const int w_lo = shift + row0 + 32 * wave, w_hi = w_lo + 31;  // positions of the wave's queries
+  const int w_lo = shift + row0 + wave0, w_hi = w_lo + 31;  // positions of the wave's queries
   // Tiles past the wave's last query are only copied for the others.
   int seen = kt.count;
   while (seen > 0 && kt.key0(seen - 1, kFwdKeys) > w_hi) --seen;
@@ -474,7 +477,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int splits) 
 template <int kHd>
 hipError_t launch(const AttnArgs &a, const AttnPlan &plan, hipStream_t stream) {
   if (!plan.split) {
-    attn_kernel<kHd><<<dim3((unsigned)((int64_t)Order(plan.slots, a.sequences, a.window).count() * a.q_heads)), dim3(64 * kFwdWaves), 0, stream>>>(a, plan.slots);
+    attn_kernel<kHd><<<dim3((unsigned)((int64_t)Order(plan.slots, a.sequences, a.window).count() * (a.q_heads / plan.pack))), dim3(64 * kFwdWaves), 0, stream>>>(a, plan.slots, plan.pack);
     return hipGetLastError();
   }
   attn_split_kernel<kHd><<<dim3((unsigned)((int64_t)plan.slots * a.k_heads * plan.splits)), dim3(64 * kSplitWaves), 0,
@@ -527,12 +530,18 @@ AttnPlan plan_attention(const puro_attention_shape &a) {
   const double per_few = a.head_dim == 128 ? 1.5 : 0.6, per_many = a.head_dim == 128 ? 1.6 : 1.3;
   const double walk_few = wf < units ? most(1) / splits : mean(1);
   const double t_few = (wf < units ? 1 : wf / units) * (4 + per_few * walk_few / (kSplitWaves * kSplitKeys));
-  const double wm = (double)a.sequences * (int64_t)((ql + kFwdRows - 1) / kFwdRows) * a.q_heads;
-  const double t_many = (wm < units ? 1 : wm / units) * (5 + per_many * (wm < units ? most(kFwdRows) : mean(kFwdRows)) / kFwdKeys);
+  // Heads that share keys share a workgroup: lower blocks see fewer keys that only some
+  // of their queries see (heads alone / in twos / in fours, us: 287 / 280 / - at 4 x 4096
+  // tokens, 194 / 186 / - at 16381 with a window of 1024, 16 and 8 heads of 128; - / 51 /
+  // 46 at 8192 with a window of 512, 16 and 4 heads of 64).
+  p.pack = group % 4 == 0 ? 4 : group % 2 == 0 ? 2 : 1;
+  const int tall = kFwdRows / p.pack;
+  const double wm = (double)a.sequences * (int64_t)((ql + tall - 1) / tall) * (a.q_heads / p.pack);
+  const double t_many = (wm < units ? 1 : wm / units) * (5 + per_many * (wm < units ? most(tall) : mean(tall)) / kFwdKeys);
 
   p.split = t_few < t_many;
   p.splits = 1;
-  p.slots = (int)(p.split ? few : a.q_tokens / kFwdRows + a.sequences);
+  p.slots = (int)(p.split ? few : a.q_tokens / tall + a.sequences);
   if (p.split && splits > 1) {
     p.splits = (int)splits;
     p.ws_bytes = (size_t)few * (size_t)a.k_heads * (size_t)splits * (size_t)kSplitRows * (size_t)(a.head_dim + 2) * 4;

@@ -17,30 +17,32 @@ __device__ __forceinline__ void wait_all_and_meet() {
 // ---------------------------------------------------------------- dq
 constexpr int kDqWaves = 4, kDqRows = 32 * kDqWaves, kDqKeys = 64;
 
-// Also writes, for the kernel below, stats[0][h][row] = lse / ln 2 (+infinity for a
+// A workgroup takes `pack` heads of a group by kDqRows / pack queries, as the forward
+// kernel does.  Also writes, for the kernel below, stats[0][h][row] = lse / ln 2 (+infinity for a
 // row that sees nothing: its P are then 0) and stats[1][h][row] = D.
 template <int kHd>
-__global__ void __launch_bounds__(64 * kDqWaves, 2) attn_dq_kernel(AttnArgs a, int slots) {
+__global__ void __launch_bounds__(64 * kDqWaves, 2) attn_dq_kernel(AttnArgs a, int slots, int pack) {
   constexpr int kTile = kTileBytes<kHd>(kDqKeys);
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2][2][kTile];
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int hk = (int)(blockIdx.x % a.k_heads);
   const int rest = (int)(blockIdx.x / a.k_heads);
-  const int h = hk * a.group + rest % a.group;
-  int slot = slots - 1 - Order(slots, a.sequences, a.window)(rest / a.group);
+  const int packs = a.group / pack, tall = kDqRows / pack;     // head packs of a group; queries of a block
+  const int h = hk * a.group + rest % packs * pack + wave * 32 / tall;
+  int slot = slots - 1 - Order(slots, a.sequences, a.window)(rest / packs);
   if (slot < 0) return;
-  const Seq sq = load_seq(a, find_seq(a.q_start, a.sequences, a.q_tokens, 1, kDqRows, slot));
-  if ((int64_t)slot * kDqRows >= sq.ql) return;
-  const int row0 = slot * kDqRows;
-  const int rows = sq.ql - row0 < kDqRows ? sq.ql - row0 : kDqRows;
+  const Seq sq = load_seq(a, find_seq(a.q_start, a.sequences, a.q_tokens, 1, tall, slot));
+  if ((int64_t)slot * tall >= sq.ql) return;
+  const int row0 = slot * tall;
+  const int rows = sq.ql - row0 < tall ? sq.ql - row0 : tall;
   const int shift = sq.kl - sq.ql;
   const KeyTiles kt = key_tiles(shift + row0, shift + row0 + rows - 1, a.window, a.sinks, kDqKeys);
 
-  const int mine = 32 * wave + (lane & 31);
+  const int wave0 = wave * 32 % tall, mine = wave0 + (lane & 31);
   const int qrow = sq.q0 + row0 + (mine < rows ? mine : rows - 1);
   const int p = shift + row0 + mine;
-  const int w_lo = shift + row0 + 32 * wave, w_hi = w_lo + 31;
+  const int w_lo = shift + row0 + wave0, w_hi = w_lo + 31;
   bf16x8 qf[kHd / 16], df[kHd / 16];
   float dd = 0.0f;
 #pragma unroll
@@ -75,7 +77,7 @@ __global__ void __launch_bounds__(64 * kDqWaves, 2) attn_dq_kernel(AttnArgs a, i
   // part of dS's own rounding, but where a row sees a handful of keys it is all there is:
   // with one key dS is 0.  Blocks with such rows first correct D by the sum of their dS,
   // which is 0 for the exact D.
-  if (kt.count > 0 && (shift + row0 < 64 || (a.window > 0 && a.window + a.sinks < 64))) {
+  if (kt.count > 0 && (shift + row0 < 128 || (a.window > 0 && a.window + a.sinks < 128))) {
     float off = 0.0f;
     copy(0, 0);
     for (int i = 0; i < kt.count; ++i) {
@@ -461,8 +463,9 @@ DkPlan plan_dk(int64_t q_tokens, int64_t k_tokens, int64_t sequences, int64_t q_
 template <int kHd>
 hipError_t launch(const AttnArgs &a, hipStream_t stream) {
   if (a.q_tokens > 0) {
-    const int slots = a.q_tokens / kDqRows + a.sequences;
-    attn_dq_kernel<kHd><<<dim3((unsigned)((int64_t)Order(slots, a.sequences, a.window).count() * a.q_heads)), dim3(64 * kDqWaves), 0, stream>>>(a, slots);
+    const int pack = a.group % 4 == 0 ? 4 : a.group % 2 == 0 ? 2 : 1, slots = a.q_tokens / (kDqRows / pack) + a.sequences;
+    attn_dq_kernel<kHd><<<dim3((unsigned)((int64_t)Order(slots, a.sequences, a.window).count() * (a.q_heads / pack))),
+                          dim3(64 * kDqWaves), 0, stream>>>(a, slots, pack);
     if (hipError_t e = hipGetLastError()) return e;
   }
   if (a.k_tokens == 0) return hipSuccess;

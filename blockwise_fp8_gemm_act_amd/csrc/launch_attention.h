@@ -74,6 +74,7 @@ struct AttnArgs {
 struct AttnPlan {
   bool split;        // the kernel for few queries: 32 (query, head) rows a tile, keys over waves and splits
   int slots;         // query tiles, empty ones included
+  int pack;          // heads of a workgroup of the kernel for many queries
   int splits;        // key ranges of a tile
   size_t ws_bytes;   // fp32 partials, when splits > 1
 };
