@@ -60,13 +60,19 @@ __global__ void __launch_bounds__(64 * kDqWaves, 2) attn_dq_kernel(AttnArgs a, i
   const TileCopy<kHd> keys(a.k + (int64_t)sq.k0 * a.ks + (int64_t)hk * kHd, a.ks);
   const TileCopy<kHd> vals(a.v + (int64_t)sq.k0 * a.vs + (int64_t)hk * kHd, a.vs);
   const uint32_t lds0 = lds_addr(lds);
-  auto copy = [&](int i, int buf) {
-    const uint32_t at = lds0 + (uint32_t)(buf * 2 * kTile);
+  // This wave's copies of tile i, a part of them at a time between the products (issued
+  // together they hold the wave for a quarter of its time).  Past the last tile that one
+  // is copied again, to a place that is not read any more.
+  constexpr int kParts = kDqKeys / kGroupRows<kHd> / kDqWaves;
+  auto copy = [&](int i, int part) {
+    const uint32_t at = lds0 + (uint32_t)((i & 1) * 2 * kTile);
+    const int t = i < kt.count ? i : kt.count - 1, g = part * kDqWaves + wave;
+    keys(kt, t, kDqKeys, g, at);
+    vals(kt, t, kDqKeys, g, at + kTile);
+  };
+  auto copy_all = [&](int i) {
 #pragma unroll
-    for (int g = wave; g < kDqKeys / kGroupRows<kHd>; g += kDqWaves) {
-      keys(kt, i, kDqKeys, g, at);
-      vals(kt, i, kDqKeys, g, at + kTile);
-    }
+    for (int part = 0; part < kParts; ++part) copy(i, part);
   };
 
   arrived(qf);
@@ -79,10 +85,10 @@ __global__ void __launch_bounds__(64 * kDqWaves, 2) attn_dq_kernel(AttnArgs a, i
   // which is 0 for the exact D.
   if (kt.count > 0 && (shift + row0 < 128 || (a.window > 0 && a.window + a.sinks < 128))) {
     float off = 0.0f;
-    copy(0, 0);
+    copy_all(0);
     for (int i = 0; i < kt.count; ++i) {
       wait_all_and_meet();
-      if (i + 1 < kt.count) copy(i + 1, (i + 1) & 1);
+      copy_all(i + 1);
       const uint32_t ktile = lds0 + (uint32_t)((i & 1) * 2 * kTile), vtile = ktile + kTile;
 #pragma unroll 1
       for (int b = 0; b < 2; ++b) {
@@ -107,22 +113,31 @@ __global__ void __launch_bounds__(64 * kDqWaves, 2) attn_dq_kernel(AttnArgs a, i
   f32x16 acc[kHd / 32];
 #pragma unroll
   for (int d = 0; d < kHd / 32; ++d) acc[d] = (f32x16){};
-  if (kt.count > 0) copy(0, 0);
-  for (int i = 0; i < kt.count; ++i) {
+  // Tiles that this wave's queries see; the others are only copied for the rest.
+  const int before = a.window > 0 ? w_lo - a.window + 1 : 0;            // first key in the wave's window
+  const int on = kt.first_n > 0 || before <= 0 ? 0 : clampi(before / kDqKeys - kt.main0, 0, kt.count);
+  int seen = kt.count;
+  while (seen > on && kt.key0(seen - 1, kDqKeys) > w_hi) --seen;
+  if (kt.count > 0) copy_all(0);
+  int i = 0;
+  for (; i < on; ++i) {
     wait_all_and_meet();
-    if (i + 1 < kt.count) copy(i + 1, (i + 1) & 1);
+    copy_all(i + 1);
+  }
+  for (; i < seen; ++i) {
+    wait_all_and_meet();
     const int key0 = kt.key0(i, kDqKeys);
     const uint32_t ktile = lds0 + (uint32_t)((i & 1) * 2 * kTile), vtile = ktile + kTile;
-    const bool none = key0 > w_hi || (a.window > 0 && key0 + kDqKeys - 1 <= w_lo - a.window && key0 >= a.sinks);
-    if (none) continue;
     const bool all = key0 + kDqKeys - 1 <= w_lo && (a.window == 0 || key0 > w_hi - a.window);
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       f32x16 s = {}, dp = {};
 #pragma unroll
       for (int kk = 0; kk < kHd / 16; ++kk) s = mfma(row_frag<kHd>(ktile, 32 * b, kk), qf[kk], s);
+      copy(i + 1, b * kParts / 2);
 #pragma unroll
       for (int kk = 0; kk < kHd / 16; ++kk) dp = mfma(row_frag<kHd>(vtile, 32 * b, kk), df[kk], dp);
+      if (kParts == 4) copy(i + 1, b * 2 + 1);
       feed<2, kHd / 8, 0>();
       if (!all) mask_tile(s, key0 + 32 * b, p, a.window, a.sinks);
 #pragma unroll
@@ -136,6 +151,11 @@ __global__ void __launch_bounds__(64 * kDqWaves, 2) attn_dq_kernel(AttnArgs a, i
       feed<2, 0, kHd / 16>();
     }
   }
+  for (; i < kt.count; ++i) {
+    wait_all_and_meet();
+    copy_all(i + 1);
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // no copy outlives its workgroup's LDS
   if (mine < rows) {
     uint16_t *out = a.dq + (int64_t)qrow * a.dqs + (int64_t)h * kHd;
 #pragma unroll
@@ -199,17 +219,16 @@ __host__ __device__ constexpr size_t part_floats() {
   return (size_t)2 * kDkRows * kHd;
 }
 
-__device__ __forceinline__ void dma4(const void *src, uint32_t lds) {
+__device__ __forceinline__ void dma4_s(const void *base, uint32_t off, uint32_t lds) {
   uint32_t save;
   asm volatile(
       "s_mov_b32 %0, m0\n\t"
-      "s_mov_b32 m0, %2\n\t"
+      "s_mov_b32 m0, %3\n\t"
       "s_nop 0\n\t"
-      "global_load_lds_dword %1, off\n\t"
+      "global_load_lds_dword %1, %2\n\t"
       "s_mov_b32 m0, %0"
       : "=&s"(save)
-      : "v"(src), "s"(lds)
-      : "memory");
+      : "v"(off), "s"(base), "s"(lds));
 }
 
 template <int kHd>
@@ -278,28 +297,37 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
   const uint32_t lds0 = lds_addr(lds), stat0 = lds_addr(stat);
   int copy_r, copy_c;
   copy_place<kHd>(copy_r, copy_c);
-  // Tiles are walked head by head; the next one to copy:
-  int next_h = hk * a.group + (tiles > 0 ? begin / tiles : 0), next_t = tiles > 0 ? begin % tiles : 0;
-  auto copy = [&](int buf) {
-    const int h = next_h, q0 = (tile0 + next_t) * kDkQueries;
-    if (++next_t == tiles) {
-      next_t = 0;
-      ++next_h;
-    }
+  // Tiles are walked head by head and copied one ahead, a part of the copies at a time
+  // between the products: issued together, a tile's copies held each wave for 2200 of the
+  // 8000 cycles that it spends on a tile.  Past the last tile that one is copied again, to
+  // a place that is not read any more.
+  constexpr int kParts = kDkQueries / kGroupRows<kHd> / kDkWaves;
+  struct Tile {
+    int h, t;
+  };
+  auto after = [&](Tile x) {
+    const bool wrap = x.t + 1 == tiles;
+    return Tile{x.h + wrap, wrap ? 0 : x.t + 1};
+  };
+  struct Source {
+    const uint16_t *q, *d;
+    int last;           // of the tile's rows in the sequence: those past it read it
+  };
+  auto source = [&](Tile x) {
+    const int q0 = (tile0 + x.t) * kDkQueries;
+    return Source{a.q + (int64_t)(sq.q0 + q0) * a.qs + (int64_t)x.h * kHd,
+                  a.d_o + (int64_t)(sq.q0 + q0) * a.os + (int64_t)x.h * kHd, sq.ql - 1 - q0};
+  };
+  auto copy = [&](const Source &from, int buf, int part) {
     const uint32_t at = lds0 + (uint32_t)(buf * 2 * kTile);
-    const int last = sq.ql - 1 - q0;                     // rows past the sequence's end: its last one
-    const uint16_t *qb = a.q + (int64_t)(sq.q0 + q0) * a.qs + (int64_t)h * kHd;
-    const uint16_t *db = a.d_o + (int64_t)(sq.q0 + q0) * a.os + (int64_t)h * kHd;
-#pragma unroll
-    for (int g = wave; g < kDkQueries / kGroupRows<kHd>; g += kDkWaves) {
-      const int r = g * kGroupRows<kHd> + copy_r;
-      const uint32_t in = (uint32_t)(r < last ? r : last);
-      dma16_s(qb, in * (uint32_t)(a.qs * 2) + copy_c * 16, at + (uint32_t)(g * kGroupBytes));
-      dma16_s(db, in * (uint32_t)(a.os * 2) + copy_c * 16, at + kTile + (uint32_t)(g * kGroupBytes));
-    }
-    if (wave < 2)
-      dma4(a.ws + (int64_t)(wave * a.q_heads + h) * a.q_tokens + sq.q0 + q0 + (lane < last ? lane : last),
-           __builtin_amdgcn_readfirstlane(stat0 + (uint32_t)((buf * 2 + wave) * kDkQueries * 4)));
+    const int g = part * kDkWaves + wave, r = g * kGroupRows<kHd> + copy_r;
+    const uint32_t in = (uint32_t)(r < from.last ? r : from.last);
+    dma16_s(from.q, in * (uint32_t)(a.qs * 2) + copy_c * 16, at + (uint32_t)(g * kGroupBytes));
+    dma16_s(from.d, in * (uint32_t)(a.os * 2) + copy_c * 16, at + kTile + (uint32_t)(g * kGroupBytes));
+  };
+  auto copy_stat = [&](Tile x, int last, int buf) {      // waves 2 and 3 copy what waves 0 and 1 do
+    dma4_s(a.ws + (int64_t)((wave & 1) * a.q_heads + x.h) * a.q_tokens + sq.q0 + (tile0 + x.t) * kDkQueries,
+           (uint32_t)((lane < last ? lane : last) * 4), stat0 + (uint32_t)((buf * 2 + (wave & 1)) * kDkQueries * 4));
   };
 
   arrived(kf);
@@ -308,35 +336,32 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
 #pragma unroll
   for (int d = 0; d < kHd / 32; ++d) dk[d] = dv[d] = (f32x16){};
   const float c2 = a.scale * kLog2e;
-  int now_t = next_t;
-  if (begin < end) copy(0);
-  for (int i = begin; i < end; ++i) {
-    const int buf = (i - begin) & 1;
-    wait_all_and_meet();
-    const int q0 = (tile0 + now_t) * kDkQueries;
-    now_t = next_t;
-    if (i + 1 < end) copy(buf ^ 1);
+  // Tiles that this wave's keys are seen from; the others are only copied for the rest.
+  const int from_q = (w_lo > first ? w_lo : first) - shift;
+  const int to_q = (a.window == 0 || w_lo < a.sinks || w_hi + a.window - 1 > final ? final : w_hi + a.window - 1) - shift;
+  const int seen_from = from_q / kDkQueries - tile0, seen_to = to_q < from_q ? 0 : to_q / kDkQueries - tile0 + 1;
+
+  auto products = [&](int q0, int buf, const Source &from) {
     const uint32_t qtile = lds0 + (uint32_t)(buf * 2 * kTile), dtile = qtile + kTile;
 #pragma unroll 1
     for (int b = 0; b < 2; ++b) {
       const int p_lo = shift + q0 + 32 * b, p_hi = p_lo + 31;
-      const bool none = p_lo > final || p_hi < first || w_lo > p_hi ||
-                        (a.window > 0 && w_hi <= p_lo - a.window && w_lo >= a.sinks);
-      if (none) continue;
       const bool all = p_lo >= first && p_hi <= final && w_hi <= p_lo &&
                        (a.window == 0 || w_lo > p_hi - a.window || w_hi < a.sinks);
       f32x16 s = {}, dp = {};
 #pragma unroll
       for (int kk = 0; kk < kHd / 16; ++kk) s = mfma(row_frag<kHd>(qtile, 32 * b, kk), kf[kk], s);
+      copy(from, buf ^ 1, b * kParts / 2);
 #pragma unroll
       for (int kk = 0; kk < kHd / 16; ++kk) dp = mfma(row_frag<kHd>(dtile, 32 * b, kk), vf[kk], dp);
+      if (kParts == 4) copy(from, buf ^ 1, b * 2 + 1);
       feed<2, kHd / 8, 0>();
       if (!all) {
-        int from = p_lo + 4 * half - seen_lo;
-        asm volatile("" : "+v"(from));      // keeps the comparisons inside this branch
+        int since = p_lo + 4 * half - seen_lo;
+        asm volatile("" : "+v"(since));      // keeps the comparisons inside this branch
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-          s[j] = (uint32_t)(from + 8 * (j / 4) + j % 4) < seen_n ? s[j] : -__builtin_inff();
+          s[j] = (uint32_t)(since + 8 * (j / 4) + j % 4) < seen_n ? s[j] : -__builtin_inff();
       }
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
@@ -360,8 +385,52 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
       }
       feed<2, 0, kHd / 8>();
     }
-  }
+  };
 
+  if (begin < end) {
+    int i = begin, buf = 0;
+    Tile now{hk * a.group + begin / tiles, begin % tiles};
+    {
+      const Source from = source(now);
+#pragma unroll
+      for (int part = 0; part < kParts; ++part) copy(from, 0, part);
+      copy_stat(now, from.last, 0);
+    }
+    while (i < end) {
+      const int stop = now.t + (end - i) < tiles ? now.t + (end - i) : tiles;     // this head's tiles of the walk
+      const int on = clampi(seen_from, now.t, stop), off = clampi(seen_to, on, stop);
+      auto turn = [&]() {
+        wait_all_and_meet();
+        const Tile next = i + 1 < end ? after(now) : now;
+        const Source from = source(next);
+        copy_stat(next, from.last, buf ^ 1);
+        return from;
+      };
+      auto done = [&]() {
+        now = i + 1 < end ? after(now) : now;
+        ++i;
+        buf ^= 1;
+      };
+      for (int t = now.t; t < on; ++t) {
+        const Source from = turn();
+#pragma unroll
+        for (int part = 0; part < kParts; ++part) copy(from, buf ^ 1, part);
+        done();
+      }
+      for (int t = on; t < off; ++t) {
+        const Source from = turn();
+        products((tile0 + t) * kDkQueries, buf, from);
+        done();
+      }
+      for (int t = off; t < stop; ++t) {
+        const Source from = turn();
+#pragma unroll
+        for (int part = 0; part < kParts; ++part) copy(from, buf ^ 1, part);
+        done();
+      }
+    }
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // no copy outlives its workgroup's LDS
   if (partial) {
     // [dk, dv][key][column]: registers 4g .. 4g+3 are 4 consecutive columns.
     float *pk = partial + mine * kHd, *pv = pk + kDkRows * kHd;
