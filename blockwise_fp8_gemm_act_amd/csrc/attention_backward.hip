@@ -115,7 +115,8 @@ __global__ void __launch_bounds__(64 * kDqWaves, 2) attn_dq_kernel(AttnArgs a, i
   for (int d = 0; d < kHd / 32; ++d) acc[d] = (f32x16){};
   // Tiles that this wave's queries see; the others are only copied for the rest.
   const int before = a.window > 0 ? w_lo - a.window + 1 : 0;            // first key in the wave's window
-  const int on = kt.first_n > 0 || before <= 0 ? 0 : clampi(before / kDqKeys - kt.main0, 0, kt.count);
+  const bool firsts = kt.first_n > 0 || kt.main0 * kDqKeys < a.sinks;   // the first tiles hold first keys
+  const int on = firsts || before <= 0 ? 0 : clampi(before / kDqKeys - kt.main0, 0, kt.count);
   int seen = kt.count;
   while (seen > on && kt.key0(seen - 1, kDqKeys) > w_hi) --seen;
   if (kt.count > 0) copy_all(0);
