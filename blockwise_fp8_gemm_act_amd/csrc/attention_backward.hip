@@ -182,7 +182,7 @@ struct DkPlan {
   size_t near_at, edge_at, far_at, floats;   // partials in the workspace, in floats: of near walks, of near walks over
                                              // first keys that are not cut, of far walks
 };
-constexpr int kFarChunk = 16;     // tiles of a far part
+constexpr int kFarChunk = 24;     // tiles of a far part: about a near walk's, whose workgroups run beside it
 
 struct Walk {
   int q_lo, q_hi;     // queries of the sequence
@@ -508,10 +508,13 @@ DkPlan plan_dk(int64_t q_tokens, int64_t k_tokens, int64_t sequences, int64_t q_
   p.slots = (int)(k_tokens / kDkRows + sequences);
   const int64_t group = q_heads / k_heads;
   const int64_t per_seq = (q_tokens + sequences - 1) / sequences;
-  // Near walks are cut, into parts of at least 8 tiles, where the blocks alone do not
-  // fill the card's 512 places (256 compute units, two workgroups each) twice.
+  // Near walks are cut, into parts of at least 8 tiles, where the blocks alone do not fill
+  // the card: 256 compute units, two workgroups each (three with heads of 64).  8191
+  // tokens in 6 sequences, window 512, 16 and 4 heads of 64, 1 / 2 / 3 / 6 parts: 141 /
+  // 118 / 126 / 128 us.
+  const int64_t places = head_dim == 128 ? 512 : 768;
   const int64_t seen = window > 0 && window + kDkRows < per_seq ? window + kDkRows : per_seq;
-  int64_t parts = 1024 / ((int64_t)p.slots * k_heads);
+  int64_t parts = places / ((int64_t)p.slots * k_heads);
   const int64_t most = (seen + kDkQueries - 1) / kDkQueries * group / 8;
   if (parts > most) parts = most;
   if (parts > 16) parts = 16;
