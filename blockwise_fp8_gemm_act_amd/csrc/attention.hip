@@ -234,12 +234,12 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 2) attn_kernel(AttnArgs a, int
 
   const float l = half_sum(st.l);
   if (mine < rows) {
-    const float f = l > 0.0f ? 1.0f / l : 0.0f;
+    const float f = l == 0.0f ? 0.0f : 1.0f / l;            // 0: nothing seen; NaN stays NaN
     uint16_t *orow = a.o + (int64_t)qrow * a.os + (int64_t)h * kHd;
 #pragma unroll
     for (int d = 0; d < kHd / 32; ++d) store_block(orow + 32 * d, st.o[d], f);
     if (a.lse && half == 0)
-      a.lse[(int64_t)h * a.q_tokens + qrow] = l > 0.0f ? (st.m + __builtin_log2f(l)) * kLn2 : -__builtin_inff();
+      a.lse[(int64_t)h * a.q_tokens + qrow] = l == 0.0f ? -__builtin_inff() : (st.m + __builtin_log2f(l)) * kLn2;
   }
 }
 
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(64 * kSplitWaves) attn_split_kernel(AttnArgs a
   }
   if (mine >= rows) return;
   if (splits == 1) {
-    const float g = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float g = sum == 0.0f ? 0.0f : 1.0f / sum;
     uint16_t *orow = a.o + (int64_t)qrow * a.os + (int64_t)h * kHd + d0;
 #pragma unroll
     for (int j = 0; j < kCols; j += 8) {
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(64 * kSplitWaves) attn_split_kernel(AttnArgs a
       *reinterpret_cast<u32x4 *>(orow + j) = w;
     }
     if (a.lse && wave == 0 && half == 0)
-      a.lse[(int64_t)h * a.q_tokens + qrow] = sum > 0.0f ? (m + __builtin_log2f(sum)) * kLn2 : -__builtin_inff();
+      a.lse[(int64_t)h * a.q_tokens + qrow] = sum == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(sum)) * kLn2;
   } else {
     float *part = a.ws + ((size_t)((size_t)tile * a.k_heads + hk) * splits + split) * split_floats<kHd>();
 #pragma unroll
@@ -464,14 +464,14 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int splits) 
       for (int j = 0; j < kPer; ++j) x[j] += one[e][j] * f;
     }
   }
-  const float g = sum > 0.0f ? 1.0f / sum : 0.0f;
+  const float g = sum == 0.0f ? 0.0f : 1.0f / sum;
   uint16_t *orow = a.o + (int64_t)qrow * a.os + (int64_t)h * kHd;
   if (kPer == 2)
     *reinterpret_cast<uint32_t *>(orow + 2 * lane) = pack_bf16(x[0] * g, x[kPer - 1] * g);
   else
     orow[lane] = (uint16_t)pack_bf16(x[0] * g, 0.0f);
   if (a.lse && lane == 0)
-    a.lse[(int64_t)h * a.q_tokens + qrow] = sum > 0.0f ? (m + __builtin_log2f(sum)) * kLn2 : -__builtin_inff();
+    a.lse[(int64_t)h * a.q_tokens + qrow] = sum == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(sum)) * kLn2;
 }
 
 template <int kHd>

@@ -279,7 +279,6 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
   const int begin = (int)(work * part / parts), end = (int)(work * (part + 1) / parts);
 
   const int mine = 32 * wave + (lane & 31);
-  const int krow = sq.k0 + key0 + (mine < keys ? mine : keys - 1);
   const int key = key0 + mine;
   const int w_lo = key0 + 32 * wave, w_hi = w_lo + 31;
   // The positions that see this lane's key in this work: seen_n of them from seen_lo.
@@ -287,6 +286,9 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
   const int seen_lo = key > first ? key : first;
   const int seen_hi = a.window == 0 || key < a.sinks || key + a.window - 1 > final ? final : key + a.window - 1;
   const uint32_t seen_n = (uint32_t)(seen_hi >= seen_lo ? seen_hi - seen_lo + 1 : 0);
+  // A key that nothing here sees reads a row that something does (the first of first keys,
+  // the last of others), so that what it holds never matters.
+  const int krow = sq.k0 + key0 + (mine < keys && seen_n > 0 ? mine : key0 < a.sinks ? 0 : keys - 1);
   bf16x8 kf[kHd / 16], vf[kHd / 16];
 #pragma unroll
   for (int kk = 0; kk < kHd / 16; ++kk) {
@@ -444,8 +446,8 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
         *reinterpret_cast<f32x4 *>(pv + c) = (f32x4){dv[d][4 * g], dv[d][4 * g + 1], dv[d][4 * g + 2], dv[d][4 * g + 3]};
       }
   } else if (mine < keys) {
-    uint16_t *ok = a.dk + (int64_t)krow * a.dks + (int64_t)hk * kHd;
-    uint16_t *ov = a.dv + (int64_t)krow * a.dvs + (int64_t)hk * kHd;
+    uint16_t *ok = a.dk + (int64_t)(sq.k0 + key) * a.dks + (int64_t)hk * kHd;
+    uint16_t *ov = a.dv + (int64_t)(sq.k0 + key) * a.dvs + (int64_t)hk * kHd;
 #pragma unroll
     for (int d = 0; d < kHd / 32; ++d) {
       store_block(ok + 32 * d, dk[d], a.scale);

@@ -338,3 +338,36 @@ def test_backward_of_first_keys_under_long_sequences(ql, window, sinks, qh, kh):
     want = ref.attention(q, k, v, seqs, window, sinks, do=do, bounds=True)
     for name, g in zip(("dq", "dk", "dv"), got):
         ref.check(g, want[name], want["b_" + name], name)
+
+
+@pytest.mark.parametrize("ql,kl,window,sinks", [([40], [400], 50, 0), ([40, 3], [400, 300], 50, 3), ([1000], [1900], 100, 4)])
+@pytest.mark.parametrize("qh,kh,hd", [(2, 1, 128), (4, 1, 64)])
+def test_backward_of_keys_that_nothing_sees(ql, kl, window, sinks, qh, kh, hd):
+    """Keys that left every query's window hold NaN: their gradients are 0, and no other one changes."""
+    q, k, v, seqs = packed(ql, kl, qh, kh, hd, 140)
+    do = normal(q.shape, 143, 1e-3)
+    gone = [slice(k0 + sinks, k0 + n - m - window + 1) for _, m, k0, n in seqs]
+    for g in gone:
+        k[g] = v[g] = 0.0
+    want = ref.attention(q, k, v, seqs, window, sinks, do=do, bounds=True)
+    for g in gone:
+        k[g] = v[g] = float("nan")
+    o, lse = puro.attention(q, k, v, starts(ql), starts(kl), window=window, sinks=sinks)
+    got = puro.attention_backward(do, q, k, v, o, lse, starts(ql), starts(kl), window=window, sinks=sinks)
+    for name, x in zip(("dq", "dk", "dv"), got):
+        ref.check(x, want[name], want["b_" + name], name)
+    for g in gone:
+        assert not bool(got[1][g].any()) and not bool(got[2][g].any())
+
+
+@pytest.mark.parametrize("heads", [2, 256])
+def test_a_query_that_is_nan(heads):
+    """Its row and its log-sum are NaN, in either kernel; the other rows keep their values."""
+    q, k, v, seqs = packed([70], [200], heads, heads, 64, 150)
+    want = ref.attention(q[:, :2], k[:, :2], v[:, :2], seqs, bounds=True)
+    q[13] = float("nan")
+    o, lse = puro.attention(q, k, v)
+    keep = [i for i in range(70) if i != 13]
+    assert bool(o[13].isnan().all()) and bool(lse[:, 13].isnan().all())
+    ref.check(o[keep, :2], want["o"][keep], want["b_o"][keep], "o")
+    ref.check(lse[:2, keep], want["lse"][:, keep], want["b_lse"][:, keep], "lse")
