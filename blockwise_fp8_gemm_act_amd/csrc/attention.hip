@@ -82,7 +82,7 @@ __device__ __forceinline__ void meet() {
 __device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 template <int kHd>
-__global__ void __launch_bounds__(64 * kFwdWaves, 2) attn_kernel(AttnArgs a, int slots, int pack) {
+__global__ void __launch_bounds__(64 * kFwdWaves, kHd == 64 ? 4 : 2) attn_kernel(AttnArgs a, int slots, int pack) {
   constexpr int kTile = kTileBytes<kHd>(kFwdKeys);
   __shared__ __attribute__((aligned(1024))) uint8_t lds[6 * kTile];     // three places of keys, three of values
   const int lane = threadIdx.x & 63, half = lane >> 5;
@@ -96,7 +96,8 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 2) attn_kernel(AttnArgs a, int
   const int h = hk * a.group + rest % packs * pack + wave * 32 / tall;
   int slot = slots - 1 - Order(slots, a.sequences, a.window)(rest / packs);
   if (slot < 0) return;
-  const Seq sq = load_seq(a, find_seq(a.q_start, a.sequences, a.q_tokens, 1, tall, slot));
+  int sequence;
+  const Seq sq = find_seq(a, a.q_start, 1, tall, slot, sequence);
   if ((int64_t)slot * tall >= sq.ql) return;
   const int shift = sq.kl - sq.ql;                              // position of query 0
   const TileCopy<kHd> keys(a.k + (int64_t)sq.k0 * a.ks + (int64_t)hk * kHd, a.ks);
@@ -177,7 +178,6 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 2) attn_kernel(AttnArgs a, int
     exps(s[1], 1);
   };
 
-  arrived(qf);
   if (kt.count > 0) {
 #pragma unroll
     for (int part = 0; part < kParts; ++part) {
@@ -188,6 +188,7 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 2) attn_kernel(AttnArgs a, int
       copy_keys(2, part);
     }
   }
+  arrived(qf);
   landed();
   meet();
   if (seen > 0) {
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 2) attn_kernel(AttnArgs a, int
   }
   for (; i < kt.count; ++i) {
     if (i + 1 == seen) {
-        values(i, 0);
+      values(i, 0);
       values(i, 1);
     }
 #pragma unroll
@@ -269,7 +270,8 @@ __global__ void __launch_bounds__(64 * kSplitWaves) attn_split_kernel(AttnArgs a
   const int rest = (int)(blockIdx.x / a.k_heads);
   const int split = rest % splits, tile = rest / splits;
   int slot = tile;
-  const Seq sq = load_seq(a, find_seq(a.q_start, a.sequences, a.q_tokens, a.group, kSplitRows, slot));
+  int sequence;
+  const Seq sq = find_seq(a, a.q_start, a.group, kSplitRows, slot, sequence);
   const int all_rows = sq.ql * a.group;
   if ((int64_t)slot * kSplitRows >= all_rows) return;
   const int row0 = slot * kSplitRows;
@@ -304,8 +306,6 @@ __global__ void __launch_bounds__(64 * kSplitWaves) attn_split_kernel(AttnArgs a
   st.clear();
   const float c2 = a.scale * kLog2e;
   const int begin = (int)((int64_t)kt.count * split / splits), end = (int)((int64_t)kt.count * (split + 1) / splits);
-  arrived(qf);                                        // only copies are counted from here on
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   // Copies run two chunks ahead, each issued as soon as its place has been read: keys
   // after the scores, values after their products.  Waiting for one tile then leaves
   // the three younger ones under way.
@@ -324,6 +324,8 @@ __global__ void __launch_bounds__(64 * kSplitWaves) attn_split_kernel(AttnArgs a
     copy_keys(i + kSplitWaves, 1);
     copy_values(i + kSplitWaves, 1);
   }
+  arrived(qf);                                        // and the copies before: from here on only copies are counted
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   for (int odd = 0; i < end; i += kSplitWaves, odd ^= 1) {
     const bool one = i + kSplitWaves < end, two = i + 2 * kSplitWaves < end;    // chunks that follow
     const int key0 = kt.key0(i, kSplitKeys);
@@ -430,7 +432,8 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int splits) 
   const int rest = (int)(blockIdx.x / a.k_heads);
   const int mine = (rest % (kSplitRows / 4)) * 4 + wave, tile = rest / (kSplitRows / 4);
   int slot = tile;
-  const Seq sq = load_seq(a, find_seq(a.q_start, a.sequences, a.q_tokens, a.group, kSplitRows, slot));
+  int sequence;
+  const Seq sq = find_seq(a, a.q_start, a.group, kSplitRows, slot, sequence);
   if ((int64_t)slot * kSplitRows + mine >= sq.ql * a.group) return;
   const int r = slot * kSplitRows + mine;
   const int qrow = sq.q0 + r / a.group, h = hk * a.group + r % a.group;
@@ -477,7 +480,8 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int splits) 
 template <int kHd>
 hipError_t launch(const AttnArgs &a, const AttnPlan &plan, hipStream_t stream) {
   if (!plan.split) {
-    attn_kernel<kHd><<<dim3((unsigned)((int64_t)Order(plan.slots, a.sequences, a.window).count() * (a.q_heads / plan.pack))), dim3(64 * kFwdWaves), 0, stream>>>(a, plan.slots, plan.pack);
+    const int64_t blocks = (int64_t)Order(plan.slots, a.sequences, a.window).count() * (a.q_heads / plan.pack);
+    attn_kernel<kHd><<<dim3((unsigned)blocks), dim3(64 * kFwdWaves), 0, stream>>>(a, plan.slots, plan.pack);
     return hipGetLastError();
   }
   attn_split_kernel<kHd><<<dim3((unsigned)((int64_t)plan.slots * a.k_heads * plan.splits)), dim3(64 * kSplitWaves), 0,
@@ -494,10 +498,11 @@ hipError_t launch(const AttnArgs &a, const AttnPlan &plan, hipStream_t stream) {
 }  // namespace
 
 // Both kernels' times are estimated from the average sequence and the smaller wins.  A
-// compute unit holds one workgroup of either, which costs a fixed time and one for each
-// 64 (128) keys it walks; the constants, in us, are fitted to 47 shapes of 1 to 64
-// sequences, 8 to 4096 queries and up to 16384 earlier keys.  Examples (many / few
-// queries' kernel, 16 and 8 heads of 128): 64 x 8 queries over 2056 keys 266 / 124 us;
+// workgroup costs a fixed time and one for each 64 (128) keys it walks, and 256 of them
+// run at a time; the constants, in us, are fitted to 47 shapes of heads of 128 and 97 of
+// heads of 64, with 1 to 64 sequences, 8 to 4096 queries and up to 16384 earlier keys (97
+// shapes: on average 0.3% slower than the better kernel, 17% at worst).  Examples (many /
+// few queries' kernel), 16 and 8 heads of 128: 64 x 8 queries over 2056 keys 266 / 124 us;
 // 16 x 64 over 2112 67 / 61; 8 x 512 over 512 34 / 66; 1 x 4096 over 4096 113 / 229;
 // 1 x 512 over 16896 755 / 192.
 AttnPlan plan_attention(const puro_attention_shape &a) {
@@ -527,9 +532,10 @@ AttnPlan plan_attention(const puro_attention_shape &a) {
   if (splits > longest) splits = longest;
   if (splits > kMostSplits) splits = kMostSplits;
   if (splits < 1) splits = 1;
-  const double per_few = a.head_dim == 128 ? 1.5 : 0.6, per_many = a.head_dim == 128 ? 1.6 : 1.3;
+  const bool wide = a.head_dim == 128;
+  const double per_few = wide ? 1.5 : 0.9, per_many = wide ? 1.6 : 1.3, start_few = wide ? 4 : 3, start_many = wide ? 5 : 6;
   const double walk_few = wf < units ? most(1) / splits : mean(1);
-  const double t_few = (wf < units ? 1 : wf / units) * (4 + per_few * walk_few / (kSplitWaves * kSplitKeys));
+  const double t_few = (wf < units ? 1 : wf / units) * (start_few + per_few * walk_few / (kSplitWaves * kSplitKeys));
   // Heads that share keys share a workgroup: lower blocks see fewer keys that only some
   // of their queries see (heads alone / in twos / in fours, us: 287 / 280 / - at 4 x 4096
   // tokens, 194 / 186 / - at 16381 with a window of 1024, 16 and 8 heads of 128; - / 51 /
@@ -537,7 +543,7 @@ AttnPlan plan_attention(const puro_attention_shape &a) {
   p.pack = group % 4 == 0 ? 4 : group % 2 == 0 ? 2 : 1;
   const int tall = kFwdRows / p.pack;
   const double wm = (double)a.sequences * (int64_t)((ql + tall - 1) / tall) * (a.q_heads / p.pack);
-  const double t_many = (wm < units ? 1 : wm / units) * (5 + per_many * (wm < units ? most(tall) : mean(tall)) / kFwdKeys);
+  const double t_many = (wm < units ? 1 : wm / units) * (start_many + per_many * (wm < units ? most(tall) : mean(tall)) / kFwdKeys);
 
   p.split = t_few < t_many;
   p.splits = 1;

@@ -21,7 +21,7 @@ constexpr int kDqWaves = 4, kDqRows = 32 * kDqWaves, kDqKeys = 64;
 // kernel does.  Also writes, for the kernel below, stats[0][h][row] = lse / ln 2 (+infinity for a
 // row that sees nothing: its P are then 0) and stats[1][h][row] = D.
 template <int kHd>
-__global__ void __launch_bounds__(64 * kDqWaves, 2) attn_dq_kernel(AttnArgs a, int slots, int pack) {
+__global__ void __launch_bounds__(64 * kDqWaves, kHd == 64 ? 4 : 2) attn_dq_kernel(AttnArgs a, int slots, int pack) {
   constexpr int kTile = kTileBytes<kHd>(kDqKeys);
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2][2][kTile];
   const int lane = threadIdx.x & 63, half = lane >> 5;
@@ -32,7 +32,8 @@ __global__ void __launch_bounds__(64 * kDqWaves, 2) attn_dq_kernel(AttnArgs a, i
   const int h = hk * a.group + rest % packs * pack + wave * 32 / tall;
   int slot = slots - 1 - Order(slots, a.sequences, a.window)(rest / packs);
   if (slot < 0) return;
-  const Seq sq = load_seq(a, find_seq(a.q_start, a.sequences, a.q_tokens, 1, tall, slot));
+  int sequence;
+  const Seq sq = find_seq(a, a.q_start, 1, tall, slot, sequence);
   if ((int64_t)slot * tall >= sq.ql) return;
   const int row0 = slot * tall;
   const int rows = sq.ql - row0 < tall ? sq.ql - row0 : tall;
@@ -43,20 +44,6 @@ __global__ void __launch_bounds__(64 * kDqWaves, 2) attn_dq_kernel(AttnArgs a, i
   const int qrow = sq.q0 + row0 + (mine < rows ? mine : rows - 1);
   const int p = shift + row0 + mine;
   const int w_lo = shift + row0 + wave0, w_hi = w_lo + 31;
-  bf16x8 qf[kHd / 16], df[kHd / 16];
-  float dd = 0.0f;
-#pragma unroll
-  for (int kk = 0; kk < kHd / 16; ++kk) {
-    const int64_t at = (int64_t)h * kHd + 16 * kk + 8 * half;
-    qf[kk] = load8(a.q + (int64_t)qrow * a.qs + at);
-    df[kk] = load8(a.d_o + (int64_t)qrow * a.os + at);
-    const bf16x8 of = load8(a.o + (int64_t)qrow * a.os + at);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dd = __builtin_fmaf((float)df[kk][j], (float)of[j], dd);
-  }
-  dd = half_sum(dd);
-  float lse2 = a.lse[(int64_t)h * a.q_tokens + qrow] * kLog2e;
-  if (lse2 == -__builtin_inff()) lse2 = __builtin_inff();
   const TileCopy<kHd> keys(a.k + (int64_t)sq.k0 * a.ks + (int64_t)hk * kHd, a.ks);
   const TileCopy<kHd> vals(a.v + (int64_t)sq.k0 * a.vs + (int64_t)hk * kHd, a.vs);
   const uint32_t lds0 = lds_addr(lds);
@@ -75,6 +62,21 @@ __global__ void __launch_bounds__(64 * kDqWaves, 2) attn_dq_kernel(AttnArgs a, i
     for (int part = 0; part < kParts; ++part) copy(i, part);
   };
 
+  if (kt.count > 0) copy_all(0);
+  bf16x8 qf[kHd / 16], df[kHd / 16];
+  float dd = 0.0f;
+#pragma unroll
+  for (int kk = 0; kk < kHd / 16; ++kk) {
+    const int64_t at = (int64_t)h * kHd + 16 * kk + 8 * half;
+    qf[kk] = load8(a.q + (int64_t)qrow * a.qs + at);
+    df[kk] = load8(a.d_o + (int64_t)qrow * a.os + at);
+    const bf16x8 of = load8(a.o + (int64_t)qrow * a.os + at);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dd = __builtin_fmaf((float)df[kk][j], (float)of[j], dd);
+  }
+  dd = half_sum(dd);
+  float lse2 = a.lse[(int64_t)h * a.q_tokens + qrow] * kLog2e;
+  if (lse2 == -__builtin_inff()) lse2 = __builtin_inff();
   arrived(qf);
   arrived(df);
   const float c2 = a.scale * kLog2e;
@@ -85,7 +87,6 @@ __global__ void __launch_bounds__(64 * kDqWaves, 2) attn_dq_kernel(AttnArgs a, i
   // which is 0 for the exact D.
   if (kt.count > 0 && (shift + row0 < 128 || (a.window > 0 && a.window + a.sinks < 128))) {
     float off = 0.0f;
-    copy_all(0);
     for (int i = 0; i < kt.count; ++i) {
       wait_all_and_meet();
       copy_all(i + 1);
@@ -104,6 +105,7 @@ __global__ void __launch_bounds__(64 * kDqWaves, 2) attn_dq_kernel(AttnArgs a, i
     }
     dd += half_sum(off);
     wait_all_and_meet();
+    copy_all(0);
   }
   if (half == 0 && mine < rows) {
     a.ws[(int64_t)h * a.q_tokens + qrow] = lse2;
@@ -119,7 +121,6 @@ __global__ void __launch_bounds__(64 * kDqWaves, 2) attn_dq_kernel(AttnArgs a, i
   const int on = firsts || before <= 0 ? 0 : clampi(before / kDqKeys - kt.main0, 0, kt.count);
   int seen = kt.count;
   while (seen > on && kt.key0(seen - 1, kDqKeys) > w_hi) --seen;
-  if (kt.count > 0) copy_all(0);
   int i = 0;
   for (; i < on; ++i) {
     wait_all_and_meet();
@@ -204,14 +205,13 @@ __device__ __forceinline__ Walk walk_of(const AttnArgs &a, const DkPlan &plan, c
 
 // Far parts are numbered over the sequences like query tiles of kFarChunk * 64 / group
 // rows; a sequence uses as many of its numbers as its far walk has chunks.
-__device__ __forceinline__ int far_first(const AttnArgs &a, int s) {
-  const int start = a.q_start ? clampi(a.q_start[s], 0, a.q_tokens) : (s == 0 ? 0 : a.q_tokens);
+__device__ __forceinline__ int far_first(const AttnArgs &a, int start, int s) {
   return (int)((int64_t)start * a.group / (kFarChunk * kDkQueries)) + s;
 }
 __device__ __forceinline__ int far_parts(const AttnArgs &a, const DkPlan &plan, const Seq &sq, int s, int slot) {
   const Walk w = walk_of(a, plan, sq, slot, true);
   const int64_t chunks = ((int64_t)w.tiles * a.group + kFarChunk - 1) / kFarChunk;
-  const int room = far_first(a, s + 1) - far_first(a, s);
+  const int room = far_first(a, sq.q0 + sq.ql, s + 1) - far_first(a, sq.q0, s);
   return (int)(chunks < room ? chunks : (room > 0 ? room : 0));
 }
 
@@ -244,10 +244,11 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
   const int far_items = plan.far_slots * plan.far_blocks;
   const bool far = rest < far_items;
   int part, parts, slot, s, number = 0;
+  Seq sq;
   if (far) {
     slot = rest % plan.far_blocks;
     part = rest / plan.far_blocks;
-    s = find_seq(a.q_start, a.sequences, a.q_tokens, a.group, kFarChunk * kDkQueries, part);
+    sq = find_seq(a, a.q_start, a.group, kFarChunk * kDkQueries, part, s);
     parts = 1;
   } else {
     rest -= far_items;
@@ -255,9 +256,8 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
     parts = plan.parts;
     slot = Order(plan.slots, a.sequences, a.window)(rest / plan.parts);
     number = slot;
-    s = find_seq(a.k_start, a.sequences, a.k_tokens, 1, kDkRows, slot);
+    sq = find_seq(a, a.k_start, 1, kDkRows, slot, s);
   }
-  const Seq sq = load_seq(a, s);
   if ((int64_t)slot * kDkRows >= sq.kl) return;
   const int fars = slot < plan.far_blocks ? far_parts(a, plan, sq, s, slot) : 0;
   float *partial = nullptr;
@@ -289,14 +289,6 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
   // A key that nothing here sees reads a row that something does (the first of first keys,
   // the last of others), so that what it holds never matters.
   const int krow = sq.k0 + key0 + (mine < keys && seen_n > 0 ? mine : key0 < a.sinks ? 0 : keys - 1);
-  bf16x8 kf[kHd / 16], vf[kHd / 16];
-#pragma unroll
-  for (int kk = 0; kk < kHd / 16; ++kk) {
-    const int64_t at = (int64_t)hk * kHd + 16 * kk + 8 * half;
-    kf[kk] = load8(a.k + (int64_t)krow * a.ks + at);
-    vf[kk] = load8(a.v + (int64_t)krow * a.vs + at);
-  }
-
   const uint32_t lds0 = lds_addr(lds), stat0 = lds_addr(stat);
   int copy_r, copy_c;
   copy_place<kHd>(copy_r, copy_c);
@@ -333,6 +325,21 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
            (uint32_t)((lane < last ? lane : last) * 4), stat0 + (uint32_t)((buf * 2 + (wave & 1)) * kDkQueries * 4));
   };
 
+  Tile now{};
+  if (begin < end) {
+    now = Tile{hk * a.group + begin / tiles, begin % tiles};
+    const Source from = source(now);
+#pragma unroll
+    for (int part = 0; part < kParts; ++part) copy(from, 0, part);
+    copy_stat(now, from.last, 0);
+  }
+  bf16x8 kf[kHd / 16], vf[kHd / 16];
+#pragma unroll
+  for (int kk = 0; kk < kHd / 16; ++kk) {
+    const int64_t at = (int64_t)hk * kHd + 16 * kk + 8 * half;
+    kf[kk] = load8(a.k + (int64_t)krow * a.ks + at);
+    vf[kk] = load8(a.v + (int64_t)krow * a.vs + at);
+  }
   arrived(kf);
   arrived(vf);
   f32x16 dk[kHd / 32], dv[kHd / 32];
@@ -392,13 +399,6 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
 
   if (begin < end) {
     int i = begin, buf = 0;
-    Tile now{hk * a.group + begin / tiles, begin % tiles};
-    {
-      const Source from = source(now);
-#pragma unroll
-      for (int part = 0; part < kParts; ++part) copy(from, 0, part);
-      copy_stat(now, from.last, 0);
-    }
     while (i < end) {
       const int stop = now.t + (end - i) < tiles ? now.t + (end - i) : tiles;     // this head's tiles of the walk
       const int on = clampi(seen_from, now.t, stop), off = clampi(seen_to, on, stop);
@@ -464,8 +464,8 @@ __global__ void __launch_bounds__(256) attn_dkdv_join_kernel(AttnArgs a, DkPlan 
   const int rest = (int)(blockIdx.x / a.k_heads);
   const int number = rest / kChunks;
   int slot = number;
-  const int s = find_seq(a.k_start, a.sequences, a.k_tokens, 1, kDkRows, slot);
-  const Seq sq = load_seq(a, s);
+  int s;
+  const Seq sq = find_seq(a, a.k_start, 1, kDkRows, slot, s);
   const int fars = slot < plan.far_blocks && (int64_t)slot * kDkRows < sq.kl ? far_parts(a, plan, sq, s, slot) : 0;
   if (plan.parts == 1 && fars == 0) return;
   const int r = (rest % kChunks) * kRows + (int)threadIdx.x / kThreads, c = 8 * ((int)threadIdx.x % kThreads);
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(256) attn_dkdv_join_kernel(AttnArgs a, DkPlan 
   else
     add(a.ws + plan.edge_at + (size_t)((s * plan.far_blocks + slot) * a.k_heads + hk) * part_floats<kHd>());
   if (fars > 0) {
-    const int f0 = far_first(a, s);
+    const int f0 = far_first(a, sq.q0, s);
     for (int p = 0; p < fars; ++p)
       add(a.ws + plan.far_at + (size_t)(((f0 + p) * plan.far_blocks + slot) * a.k_heads + hk) * part_floats<kHd>());
   }

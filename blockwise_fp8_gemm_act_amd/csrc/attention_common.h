@@ -64,38 +64,39 @@ struct Seq {
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
 
+// Tiles of `unit` rows are numbered over all sequences without a prefix sum: sequence
+// s owns the numbers from start(s) * mul / unit + s up to that of s + 1, `start` being
+// q_start or k_start.  These are never fewer than its tiles; the surplus ones are empty.
+// Returns the sequence (and its number) of tile `slot` and subtracts its first number.
+//
 // Starts and lengths come from device memory: clamped, so that no row outside the
-// tensors is ever addressed.
-__device__ __forceinline__ Seq load_seq(const AttnArgs &a, int s) {
-  Seq r;
-  if (!a.q_start) return Seq{0, a.q_tokens, 0, a.k_len ? clampi(a.k_len[0], 0, a.k_tokens) : a.k_tokens};
-  r.q0 = clampi(a.q_start[s], 0, a.q_tokens);
-  r.ql = clampi(a.q_start[s + 1], r.q0, a.q_tokens) - r.q0;
-  r.k0 = clampi(a.k_start[s], 0, a.k_tokens);
-  r.kl = clampi(a.k_start[s + 1], r.k0, a.k_tokens) - r.k0;
-  if (a.k_len) r.kl = clampi(a.k_len[s], 0, r.kl);
-  return r;
-}
-
-// Tiles of `unit` rows are numbered over all sequences without a prefix sum:
-// sequence s owns the numbers from start(s) * mul / unit + s up to that of s + 1.
-// These are never fewer than its tiles; the surplus ones are empty.  Returns the
-// sequence of tile `slot` and subtracts its first number.
-__device__ __forceinline__ int find_seq(const int32_t *start, int sequences, int tokens, int mul, int unit, int &slot) {
-  if (!start) return 0;
+// tensors is ever addressed.  63 sequences at a time, one a lane and the next one's
+// start in the lane beside, so that everything is there after one latency.
+__device__ __forceinline__ Seq find_seq(const AttnArgs &a, const int32_t *start, int mul, int unit, int &slot, int &s) {
+  s = 0;
+  if (!start) return Seq{0, a.q_tokens, 0, a.k_len ? clampi(a.k_len[0], 0, a.k_tokens) : a.k_tokens};
   const int lane = threadIdx.x & 63;
-  int s = 0, first = 0;
-  for (int b = 0; b < sequences; b += 64) {
-    const int i = b + lane;
-    const int base = i < sequences ? (int)((int64_t)clampi(start[i], 0, tokens) * mul / unit) + i : 0x7fffffff;
+  const bool over_q = start == a.q_start;
+  int first = 0, q0 = 0, q1 = 0, k0 = 0, k1 = 0, kl = 0;
+  for (int b = 0; b < a.sequences; b += 63) {
+    const int i = b + lane, in = i < a.sequences ? i : a.sequences;
+    const int qs = clampi(a.q_start[in], 0, a.q_tokens), ks = clampi(a.k_start[in], 0, a.k_tokens);
+    const int len = a.k_len ? a.k_len[in < a.sequences ? in : a.sequences - 1] : a.k_tokens;
+    const int base = i < a.sequences && lane < 63 ? (int)((int64_t)(over_q ? qs : ks) * mul / unit) + i : 0x7fffffff;
     const uint64_t le = __ballot(base <= slot);
     if (!le) break;
     const int n = 63 - __builtin_clzll(le);
     s = b + n;
     first = __builtin_amdgcn_readlane(base, n);
+    q0 = __builtin_amdgcn_readlane(qs, n);
+    q1 = __builtin_amdgcn_readlane(qs, n + 1);
+    k0 = __builtin_amdgcn_readlane(ks, n);
+    k1 = __builtin_amdgcn_readlane(ks, n + 1);
+    kl = __builtin_amdgcn_readlane(len, n);
   }
   slot -= first;
-  return s;
+  const int most = k1 > k0 ? k1 - k0 : 0;
+  return Seq{q0, q1 > q0 ? q1 - q0 : 0, k0, clampi(kl, 0, most)};
 }
 
 // Order in which tiles start.  Without a window a tile's work grows along its sequence:
@@ -121,7 +122,6 @@ struct KeyTiles {
   int first_n, main0, count;    // tiles of the first keys; first tile of the window; all
   int lo, hi, sinks;
   __device__ __forceinline__ int key0(int i, int unit) const { return (i < first_n ? i : main0 + i - first_n) * unit; }
-  __device__ __forceinline__ int row(int key) const { return key < sinks ? key : clampi(key, lo, hi); }
 };
 
 __device__ __forceinline__ KeyTiles key_tiles(int p_lo, int p_hi, int window, int sinks, int unit) {
@@ -153,25 +153,11 @@ constexpr int kGroupBytes = 1024 + 16;
 template <int kHd>
 constexpr int kTileBytes(int rows) { return rows / kGroupRows<kHd> * kGroupBytes; }
 
-// Global -> LDS copy of 16 bytes a lane to lds + 16 lane.  Asm, so that the
-// compiler does not make every later LDS read wait for it: completion is awaited
-// explicitly.
-__device__ __forceinline__ void dma16(const void *src, uint32_t lds) {
-  uint32_t save;
-  asm volatile(
-      "s_mov_b32 %0, m0\n\t"
-      "s_mov_b32 m0, %2\n\t"
-      "s_nop 0\n\t"
-      "global_load_lds_dwordx4 %1, off\n\t"
-      "s_mov_b32 m0, %0"
-      : "=&s"(save)
-      : "v"(src), "s"(lds)
-      : "memory");
-}
-
-// The same from a uniform base and a 32-bit offset of the lane.  Without a memory
-// clobber, so that reads of other tiles may be scheduled around it: what it writes is
-// read only after a barrier that has one, and what it overwrites was read before one.
+// Global -> LDS copy of 16 bytes a lane to lds + 16 lane, from a uniform base and a
+// 32-bit offset of the lane.  Asm, so that the compiler does not make every later LDS read
+// wait for it: completion is awaited explicitly.  Without a memory clobber, so that reads
+// of other tiles may be scheduled around it: what it writes is read only after a barrier
+// that has one, and what it overwrites was read before one.
 __device__ __forceinline__ void dma16_s(const void *base, uint32_t off, uint32_t lds) {
   uint32_t save;
   asm volatile(
@@ -199,15 +185,6 @@ __device__ __forceinline__ void copy_place(int &r, int &c) {
     r = ((lane >> 2) & 3) + 4 * (lane >> 5);
     c = 4 * ((lane >> 4) & 1) + (lane & 3);
   }
-}
-
-// Copies group g of a tile; src_row(r) gives the global row that tile row r holds.
-template <int kHd, typename F>
-__device__ __forceinline__ void copy_group(uint32_t tile, int g, F src_row) {
-  int r, c;
-  copy_place<kHd>(r, c);
-  dma16(src_row(g * kGroupRows<kHd> + r) + 8 * c,
-        __builtin_amdgcn_readfirstlane(tile + (uint32_t)(g * kGroupBytes)));
 }
 
 // Copies of key (or value) tiles of `unit` keys, group by group and without branches:
