@@ -100,8 +100,10 @@ __global__ void __launch_bounds__(64 * kFwdWaves, kHd == 64 ? 4 : 2) attn_kernel
   const Seq sq = find_seq(a, a.q_start, 1, tall, slot, sequence);
   if ((int64_t)slot * tall >= sq.ql) return;
   const int shift = sq.kl - sq.ql;                              // position of query 0
-  const TileCopy<kHd> keys(a.k + (int64_t)sq.k0 * a.ks + (int64_t)hk * kHd, a.ks);
-  const TileCopy<kHd> vals(a.v + (int64_t)sq.k0 * a.vs + (int64_t)hk * kHd, a.vs);
+  typedef TileStream<kHd, kFwdKeys, kFwdWaves> Stream;
+  constexpr int kParts = Stream::kParts;
+  Stream keys(a.k + (int64_t)sq.k0 * a.ks + (int64_t)hk * kHd, a.ks, wave);
+  Stream vals(a.v + (int64_t)sq.k0 * a.vs + (int64_t)hk * kHd, a.vs, wave);
   const uint32_t lds0 = lds_addr(lds);
   const float c2 = a.scale * kLog2e;
 
@@ -120,31 +122,15 @@ __global__ void __launch_bounds__(64 * kFwdWaves, kHd == 64 ? 4 : 2) attn_kernel
   for (int kk = 0; kk < kHd / 16; ++kk)
     qf[kk] = load8(a.q + (int64_t)qrow * a.qs + (int64_t)h * kHd + 16 * kk + 8 * half);
 
-  // Opaque, so that a read's address stays one register plus a constant.
-  auto place = [&](int n) {
-    uint32_t at = lds0 + (uint32_t)(n * kTile);
-    asm("" : "+s"(at));
-    return at;
-  };
-  auto key_place = [&](int i) { return place(i % 3); };
-  auto value_place = [&](int i) { return place(3 + i % 3); };
-  // This wave's part of a tile's copies, in kParts groups.  Past the last tile that one
-  // is copied again, to a place that is not read any more.
-  constexpr int kParts = kFwdKeys / kGroupRows<kHd> / kFwdWaves;
-  auto copy_keys = [&](int i, int part) {
-    keys(kt, i < kt.count ? i : kt.count - 1, kFwdKeys, part * kFwdWaves + wave, key_place(i));
-  };
-  auto copy_values = [&](int i, int part) {
-    vals(kt, i < kt.count ? i : kt.count - 1, kFwdKeys, part * kFwdWaves + wave, value_place(i));
-  };
-
+  // Places of the tiles i, i + 1 and i + 2, those of keys first; turned with i.
+  uint32_t place[3] = {lds0, lds0 + kTile, lds0 + 2 * kTile};
+  constexpr int kValues = 3 * kTile;
   Row<kHd> st;
   st.clear();
   f32x16 s[2];
   bf16x8 pf[2][2];
-  auto score = [&](int i, int b) { s[b] = score_tile<kHd>(key_place(i), 32 * b, qf); };
-  auto values = [&](int i, int b) {
-    const uint32_t vtile = value_place(i);
+  auto score = [&](uint32_t ktile, int b) { s[b] = score_tile<kHd>(ktile, 32 * b, qf); };
+  auto values = [&](uint32_t vtile, int b) {
 #pragma unroll
     for (int step = 0; step < 2; ++step)
 #pragma unroll
@@ -180,20 +166,26 @@ __global__ void __launch_bounds__(64 * kFwdWaves, kHd == 64 ? 4 : 2) attn_kernel
 
   if (kt.count > 0) {
 #pragma unroll
-    for (int part = 0; part < kParts; ++part) {
-      copy_keys(0, part);
-      copy_values(0, part);
-      copy_keys(1, part);
-      copy_values(1, part);
-      copy_keys(2, part);
+    for (int t = 0; t < 3; ++t) {
+      keys.aim(kt, t);
+      keys.aim_rows(kt, t);
+      vals.aim(kt, t);
+      vals.aim_rows(kt, t);
+#pragma unroll
+      for (int part = 0; part < kParts; ++part) {
+        keys.copy(part, place[t]);
+        if (t < 2) vals.copy(part, place[t] + kValues);
+      }
     }
+    keys.aim(kt, 3);
+    keys.aim_rows(kt, 3);
   }
   arrived(qf);
   landed();
   meet();
   if (seen > 0) {
-    score(0, 0);
-    score(0, 1);
+    score(place[0], 0);
+    score(place[0], 1);
     if (!late) softmax(0);
   }
   meet();
@@ -202,31 +194,49 @@ __global__ void __launch_bounds__(64 * kFwdWaves, kHd == 64 ? 4 : 2) attn_kernel
     meet();
   }
   int i = 0;
+  // To the next tile: bases and places, then the rows.
+  auto turn = [&]() {
+    keys.aim(kt, i + 4);
+    vals.aim(kt, i + 3);
+    const uint32_t p = place[0];
+    place[0] = place[1];
+    place[1] = place[2];
+    place[2] = p;
+  };
+  auto turn_rows = [&]() {
+    keys.aim_rows(kt, i + 4);
+    vals.aim_rows(kt, i + 3);
+  };
   for (; i + 1 < seen; ++i) {
-    score(i + 1, 0);
-    copy_keys(i + 3, 0);
-    score(i + 1, 1);
-    copy_values(i + 2, 0);
-    values(i, 0);
-    if (kParts > 1) copy_keys(i + 3, kParts - 1);
-    values(i, 1);
-    if (kParts > 1) copy_values(i + 2, kParts - 1);
+    const uint32_t ktile = place[1], vtile = place[0] + kValues;
+    score(ktile, 0);
+    keys.copy(0, place[0]);
+    score(ktile, 1);
+    vals.copy(0, place[2] + kValues);
+    values(vtile, 0);
+    if (kParts > 1) keys.copy(kParts - 1, place[0]);
+    values(vtile, 1);
+    if (kParts > 1) vals.copy(kParts - 1, place[2] + kValues);
+    turn();
     feed<4, kHd / 8, kHd / 8>();
     meet();
     softmax(i + 1);
+    turn_rows();
     landed();
     meet();
   }
   for (; i < kt.count; ++i) {
     if (i + 1 == seen) {
-      values(i, 0);
-      values(i, 1);
+      values(place[0] + kValues, 0);
+      values(place[0] + kValues, 1);
     }
 #pragma unroll
     for (int part = 0; part < kParts; ++part) {
-      copy_keys(i + 3, part);
-      copy_values(i + 2, part);
+      keys.copy(part, place[0]);
+      vals.copy(part, place[2] + kValues);
     }
+    turn();
+    turn_rows();
     meet();
     landed();
     meet();

@@ -211,6 +211,54 @@ struct TileCopy {
   }
 };
 
+// The same for a loop whose products must not wait for addresses: the next tile's are
+// worked out ahead of its turn, the base beside the products (scalars only) and a lane's
+// offsets where there is time; copy() then is one instruction and its LDS address.  Only
+// tiles with rows that no query of the block sees need offsets of their own: those of the
+// first keys, the first of the window and the last.  A wave copies kParts groups of a tile.
+template <int kHd, int kUnit, int kWaves>
+struct TileStream {
+  static constexpr int kParts = kUnit / kGroupRows<kHd> / kWaves;
+  const uint16_t *base, *at;
+  uint32_t bytes;        // of a row's stride
+  int row, wave;
+  uint32_t chunk, plain[kParts], off[kParts];
+  __device__ __forceinline__ TileStream(const uint16_t *base, int64_t stride, int wave)
+      : base(base), bytes((uint32_t)(stride * 2)), wave(wave) {
+    int c;
+    copy_place<kHd>(row, c);
+    chunk = (uint32_t)(c * 16);
+    row += wave * kGroupRows<kHd>;
+#pragma unroll
+    for (int part = 0; part < kParts; ++part) plain[part] = (uint32_t)(row + part * kWaves * kGroupRows<kHd>) * bytes + chunk;
+  }
+  // Past the last tile: that one again.
+  static __device__ __forceinline__ int upto(const KeyTiles &kt, int i) { return i < kt.count ? i : kt.count - 1; }
+  __device__ __forceinline__ void aim(const KeyTiles &kt, int i) {
+    at = reinterpret_cast<const uint16_t *>(reinterpret_cast<const char *>(base) +
+                                            (uint64_t)(uint32_t)kt.key0(upto(kt, i), kUnit) * bytes);
+  }
+  __device__ __forceinline__ void aim_rows(const KeyTiles &kt, int i) {
+    i = upto(kt, i);
+#pragma unroll
+    for (int part = 0; part < kParts; ++part) off[part] = plain[part];
+    if (i <= kt.first_n || i == kt.count - 1) {
+      const int key0 = kt.key0(i, kUnit);
+      const bool first = i < kt.first_n;
+#pragma unroll
+      for (int part = 0; part < kParts; ++part) {
+        const int key = key0 + row + part * kWaves * kGroupRows<kHd>;
+        const int in = key < kt.sinks ? key : clampi(key, first ? 0 : kt.lo, first ? kt.sinks - 1 : kt.hi);
+        off[part] = (uint32_t)(in - key0) * bytes + chunk;
+        asm volatile("" : "+v"(off[part]));      // a branch, not a choice of values
+      }
+    }
+  }
+  __device__ __forceinline__ void copy(int part, uint32_t tile) const {
+    dma16_s(at, off[part], tile + (uint32_t)((part * kWaves + wave) * kGroupBytes));
+  }
+};
+
 typedef __attribute__((address_space(3))) bf16x8 lds_bf16x8;
 typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
 

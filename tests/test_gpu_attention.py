@@ -371,3 +371,20 @@ def test_a_query_that_is_nan(heads):
     assert bool(o[13].isnan().all()) and bool(lse[:, 13].isnan().all())
     ref.check(o[keep, :2], want["o"][keep], want["b_o"][keep], "o")
     ref.check(lse[:2, keep], want["lse"][:, keep], want["b_lse"][:, keep], "lse")
+
+
+@pytest.mark.parametrize("n", [62, 63, 64, 127, 200])
+def test_many_sequences(n):
+    """Short and empty sequences in numbers around what one lookup step covers."""
+    g = torch.Generator().manual_seed(160 + n)
+    ql = torch.randint(0, 5, (n,), generator=g).tolist()
+    ql[-1] = 3
+    kl = [m + e for m, e in zip(ql, torch.randint(0, 40, (n,), generator=g).tolist())]
+    q, k, v, seqs = packed(ql, kl, 2, 1, 64, 161)
+    do = normal(q.shape, 164, 1e-3)
+    o, lse = puro.attention(q, k, v, starts(ql), starts(kl))
+    check_forward(q, k, v, seqs, (o, lse))
+    got = puro.attention_backward(do, q, k, v, o, lse, starts(ql), starts(kl))
+    want = ref.attention(q, k, v, seqs, do=do, bounds=True)
+    for name, x in zip(("dq", "dk", "dv"), got):
+        ref.check(x, want[name], want["b_" + name], name)
