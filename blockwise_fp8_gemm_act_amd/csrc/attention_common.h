@@ -206,7 +206,7 @@ struct TileCopy {
     const bool first = i < kt.first_n;
     const int key = key0 + g * kGroupRows<kHd> + row;
     const int in = key < kt.sinks ? key : clampi(key, first ? 0 : kt.lo, first ? kt.sinks - 1 : kt.hi);
-    dma16_s(base + (int64_t)key0 * stride, (uint32_t)(in - key0) * (uint32_t)(stride * 2) + chunk,
+    dma16_s(base + (int64_t)key0 * stride, __umul24(in - key0, (uint32_t)(stride * 2)) + chunk,
             tile + (uint32_t)(g * kGroupBytes));
   }
 };
@@ -222,15 +222,13 @@ struct TileStream {
   const uint16_t *base, *at;
   uint32_t bytes;        // of a row's stride
   int row, wave;
-  uint32_t chunk, plain[kParts], off[kParts];
+  uint32_t chunk, off[kParts];
   __device__ __forceinline__ TileStream(const uint16_t *base, int64_t stride, int wave)
       : base(base), bytes((uint32_t)(stride * 2)), wave(wave) {
     int c;
     copy_place<kHd>(row, c);
     chunk = (uint32_t)(c * 16);
     row += wave * kGroupRows<kHd>;
-#pragma unroll
-    for (int part = 0; part < kParts; ++part) plain[part] = (uint32_t)(row + part * kWaves * kGroupRows<kHd>) * bytes + chunk;
   }
   // Past the last tile: that one again.
   static __device__ __forceinline__ int upto(const KeyTiles &kt, int i) { return i < kt.count ? i : kt.count - 1; }
@@ -241,7 +239,7 @@ struct TileStream {
   __device__ __forceinline__ void aim_rows(const KeyTiles &kt, int i) {
     i = upto(kt, i);
 #pragma unroll
-    for (int part = 0; part < kParts; ++part) off[part] = plain[part];
+    for (int part = 0; part < kParts; ++part) off[part] = __umul24(row + part * kWaves * kGroupRows<kHd>, bytes) + chunk;
     if (i <= kt.first_n || i == kt.count - 1) {
       const int key0 = kt.key0(i, kUnit);
       const bool first = i < kt.first_n;
@@ -249,7 +247,7 @@ struct TileStream {
       for (int part = 0; part < kParts; ++part) {
         const int key = key0 + row + part * kWaves * kGroupRows<kHd>;
         const int in = key < kt.sinks ? key : clampi(key, first ? 0 : kt.lo, first ? kt.sinks - 1 : kt.hi);
-        off[part] = (uint32_t)(in - key0) * bytes + chunk;
+        off[part] = __umul24(in - key0, bytes) + chunk;     // 64 rows, below 2^24 bytes each
         asm volatile("" : "+v"(off[part]));      // a branch, not a choice of values
       }
     }
