@@ -185,7 +185,7 @@ puro::AttnArgs attention_args(const puro_attention_shape &s, const uint16_t *q, 
   return a;
 }
 
-bool scale_ok(float s) { return s > 0.0f && std::isfinite(s); }
+bool scale_ok(float s) { return s >= 1e-30f && std::isfinite(s); }      // so that lse / scale stays finite
 
 }  // namespace
 

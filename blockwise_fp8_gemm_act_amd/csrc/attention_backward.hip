@@ -14,12 +14,20 @@ __device__ __forceinline__ void wait_all_and_meet() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
+__device__ __forceinline__ f32x16 splat(float x) {
+  f32x16 v;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] = x;
+  return v;
+}
+
 // ---------------------------------------------------------------- dq
 constexpr int kDqWaves = 4, kDqRows = 32 * kDqWaves, kDqKeys = 64;
 
 // A workgroup takes `pack` heads of a group by kDqRows / pack queries, as the forward
-// kernel does.  Also writes, for the kernel below, stats[0][h][row] = lse / ln 2 (+infinity for a
-// row that sees nothing: its P are then 0) and stats[1][h][row] = D.
+// kernel does.  Also writes, for the kernel below, stats[0][h][row] = -lse / scale (-infinity
+// for a row that sees nothing: its P are then 0) and stats[1][h][row] = -D: the products q k
+// and do v start from these, so that exp2(c2 sum) is P and P times the other sum dS.
 template <int kHd>
 __global__ void __launch_bounds__(64 * kDqWaves, kHd == 64 ? 4 : 2) attn_dq_kernel(AttnArgs a, int slots, int pack) {
   constexpr int kTile = kTileBytes<kHd>(kDqKeys);
@@ -75,8 +83,8 @@ __global__ void __launch_bounds__(64 * kDqWaves, kHd == 64 ? 4 : 2) attn_dq_kern
     for (int j = 0; j < 8; ++j) dd = __builtin_fmaf((float)df[kk][j], (float)of[j], dd);
   }
   dd = half_sum(dd);
-  float lse2 = a.lse[(int64_t)h * a.q_tokens + qrow] * kLog2e;
-  if (lse2 == -__builtin_inff()) lse2 = __builtin_inff();
+  const float lse = a.lse[(int64_t)h * a.q_tokens + qrow];
+  const float sd = lse == -__builtin_inff() ? lse : -lse / a.scale;
   arrived(qf);
   arrived(df);
   const float c2 = a.scale * kLog2e;
@@ -93,14 +101,14 @@ __global__ void __launch_bounds__(64 * kDqWaves, kHd == 64 ? 4 : 2) attn_dq_kern
       const uint32_t ktile = lds0 + (uint32_t)((i & 1) * 2 * kTile), vtile = ktile + kTile;
 #pragma unroll 1
       for (int b = 0; b < 2; ++b) {
-        f32x16 s = {}, dp = {};
+        f32x16 s = splat(sd), dp = {};
 #pragma unroll
         for (int kk = 0; kk < kHd / 16; ++kk) s = mfma(row_frag<kHd>(ktile, 32 * b, kk), qf[kk], s);
 #pragma unroll
         for (int kk = 0; kk < kHd / 16; ++kk) dp = mfma(row_frag<kHd>(vtile, 32 * b, kk), df[kk], dp);
         mask_tile(s, kt.key0(i, kDqKeys) + 32 * b, p, a.window, a.sinks);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) off += __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], c2, -lse2)) * (dp[j] - dd);
+        for (int j = 0; j < 16; ++j) off += __builtin_amdgcn_exp2f(s[j] * c2) * (dp[j] - dd);
       }
     }
     dd += half_sum(off);
@@ -108,10 +116,18 @@ __global__ void __launch_bounds__(64 * kDqWaves, kHd == 64 ? 4 : 2) attn_dq_kern
     copy_all(0);
   }
   if (half == 0 && mine < rows) {
-    a.ws[(int64_t)h * a.q_tokens + qrow] = lse2;
-    a.ws[(int64_t)(a.q_heads + h) * a.q_tokens + qrow] = dd;
+    a.ws[(int64_t)h * a.q_tokens + qrow] = sd;
+    a.ws[(int64_t)(a.q_heads + h) * a.q_tokens + qrow] = -dd;
   }
 
+  // Starting values kept in registers, where there are enough of them.
+  constexpr bool kKept = kHd == 128;
+  f32x16 s0, dp0;
+  if (kKept) {
+    s0 = splat(sd);
+    dp0 = splat(-dd);
+    asm volatile("" : "+v"(s0), "+v"(dp0));
+  }
   f32x16 acc[kHd / 32];
 #pragma unroll
   for (int d = 0; d < kHd / 32; ++d) acc[d] = (f32x16){};
@@ -134,6 +150,10 @@ __global__ void __launch_bounds__(64 * kDqWaves, kHd == 64 ? 4 : 2) attn_dq_kern
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       f32x16 s = {}, dp = {};
+      if (kKept) {
+        s = s0;
+        dp = dp0;
+      }
 #pragma unroll
       for (int kk = 0; kk < kHd / 16; ++kk) s = mfma(row_frag<kHd>(ktile, 32 * b, kk), qf[kk], s);
       copy(i + 1, b * kParts / 2);
@@ -143,7 +163,9 @@ __global__ void __launch_bounds__(64 * kDqWaves, kHd == 64 ? 4 : 2) attn_dq_kern
       feed<2, kHd / 8, 0>();
       if (!all) mask_tile(s, key0 + 32 * b, p, a.window, a.sinks);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) s[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], c2, -lse2)) * (dp[j] - dd);
+      for (int j = 0; j < 16; ++j)
+        s[j] = kKept ? __builtin_amdgcn_exp2f(s[j] * c2) * dp[j]
+                     : __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], c2, sd * c2)) * (dp[j] - dd);
 #pragma unroll
       for (int step = 0; step < 2; ++step) {
         const bf16x8 sf = pack_step(s, step);
@@ -317,8 +339,8 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
     const uint32_t at = lds0 + (uint32_t)(buf * 2 * kTile);
     const int g = part * kDkWaves + wave, r = g * kGroupRows<kHd> + copy_r;
     const uint32_t in = (uint32_t)(r < from.last ? r : from.last);
-    dma16_s(from.q, in * (uint32_t)(a.qs * 2) + copy_c * 16, at + (uint32_t)(g * kGroupBytes));
-    dma16_s(from.d, in * (uint32_t)(a.os * 2) + copy_c * 16, at + kTile + (uint32_t)(g * kGroupBytes));
+    dma16_s(from.q, __umul24(in, (uint32_t)(a.qs * 2)) + copy_c * 16, at + (uint32_t)(g * kGroupBytes));
+    dma16_s(from.d, __umul24(in, (uint32_t)(a.os * 2)) + copy_c * 16, at + kTile + (uint32_t)(g * kGroupBytes));
   };
   auto copy_stat = [&](Tile x, int last, int buf) {      // waves 2 and 3 copy what waves 0 and 1 do
     dma4_s(a.ws + (int64_t)((wave & 1) * a.q_heads + x.h) * a.q_tokens + sq.q0 + (tile0 + x.t) * kDkQueries,
@@ -358,7 +380,17 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
       const int p_lo = shift + q0 + 32 * b, p_hi = p_lo + 31;
       const bool all = p_lo >= first && p_hi <= final && w_hi <= p_lo &&
                        (a.window == 0 || w_lo > p_hi - a.window || w_hi < a.sinks);
-      f32x16 s = {}, dp = {};
+      f32x16 s, dp;
+#pragma unroll
+      for (int j = 0; j < 16; j += 4) {
+        const f32x4 s4 = *reinterpret_cast<const f32x4 *>(&stat[buf][0][32 * b + 2 * j + 4 * half]);
+        const f32x4 d4 = *reinterpret_cast<const f32x4 *>(&stat[buf][1][32 * b + 2 * j + 4 * half]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[j + e] = s4[e];
+          dp[j + e] = d4[e];
+        }
+      }
 #pragma unroll
       for (int kk = 0; kk < kHd / 16; ++kk) s = mfma(row_frag<kHd>(qtile, 32 * b, kk), kf[kk], s);
       copy(from, buf ^ 1, b * kParts / 2);
@@ -374,15 +406,9 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
           s[j] = (uint32_t)(since + 8 * (j / 4) + j % 4) < seen_n ? s[j] : -__builtin_inff();
       }
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const f32x4 lse2 = *reinterpret_cast<const f32x4 *>(&stat[buf][0][32 * b + 8 * g + 4 * half]);
-        const f32x4 dd = *reinterpret_cast<const f32x4 *>(&stat[buf][1][32 * b + 8 * g + 4 * half]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int j = 4 * g + e;
-          s[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], c2, -lse2[e]));
-          dp[j] = s[j] * (dp[j] - dd[e]);
-        }
+      for (int j = 0; j < 16; ++j) {
+        s[j] = __builtin_amdgcn_exp2f(s[j] * c2);
+        dp[j] *= s[j];
       }
 #pragma unroll
       for (int step = 0; step < 2; ++step) {

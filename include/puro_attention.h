@@ -169,7 +169,7 @@ typedef struct {
                            gives right results; 0: taken as k_tokens / sequences */
     int64_t window;     /* >= 0; 0: no window */
     int64_t sinks;      /* >= 0: first keys that stay visible outside the window */
-    float scale;        /* of q . k: finite, > 0 */
+    float scale;        /* of q . k: finite, at least 1e-30 */
 } puro_attention_shape;
 
 /* Device workspace of puro_attention and of puro_attention_backward for a shape (0: none; a shape that the call
