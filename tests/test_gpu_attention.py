@@ -388,3 +388,14 @@ def test_many_sequences(n):
     want = ref.attention(q, k, v, seqs, do=do, bounds=True)
     for name, x in zip(("dq", "dk", "dv"), got):
         ref.check(x, want[name], want["b_" + name], name)
+
+
+@pytest.mark.parametrize("at,by", [(0, 40.0), (64, 40.0), (70, 400.0), (127, 4000.0), (320, 400.0)])
+@pytest.mark.parametrize("heads", [2, 256])
+def test_a_score_that_outgrows_the_others(heads, at, by):
+    """One key far above all before and after it, up to where exp(s - running maximum) leaves fp32."""
+    q, k, v, seqs = packed([100], [400], heads, heads, 64, 170, std=0.1)
+    q[:, :, 0] = 1.0
+    k[at, :, 0] = by
+    got = puro.attention(q, k, v, scale=1.0)
+    check_forward(q[:, :2], k[:, :2], v[:, :2], seqs, (got[0][:, :2], got[1][:2]), scale=1.0)
