@@ -60,7 +60,12 @@ constexpr int kFwdWaves = 8, kFwdKeys = 64;
 // (query, head) rows of a workgroup; `pack` heads of a group by kFwdRows / pack queries.
 constexpr int kFwdRows = 32 * kFwdWaves;
 
-// The two waves of a SIMD take turns: while one multiplies (scores of the next tile,
+// Bound by the matrix cores: 4 head_dim operations a visible pair, against 2 bytes of
+// keys and values that a block reads for every 256 of its rows.  Beside them an
+// exponential and four other vector operations a pair want as long as the products at
+// heads of 128, and one wave alone issues them at half rate.
+//
+// So the two waves of a SIMD take turns: while one multiplies (scores of the next tile,
 // values of this one), the other does the softmax of its next tile, with a barrier
 // between the turns.  Waves 4-7 run one turn behind waves 0-3.
 //
@@ -72,8 +77,18 @@ constexpr int kFwdRows = 32 * kFwdWaves;
 // products starts copies of the keys of tile i+3 and the values of tile i+2, each wave
 // its part; they are awaited a turn later, at the end of softmax i+1, and needed two
 // turns after that.  With three places each for keys and values, the places they take
-// were read for the last time two turns before.  (Issued together, a tile's copies
-// stall their wave for 700 to 1000 cycles, as long as the softmax.)
+// were read for the last time two turns before.
+//
+// What it took, at 4 x 4096 tokens, 16 and 8 heads of 128 (275 GFLOP, us): waves that run
+// freely 342; turns 289; copies spread between the products (together they stall their
+// wave as long as the softmax) and heads that share keys in one block 278; addresses of
+// the copies worked out a turn ahead (a turn's products issue 200 other instructions
+// instead of 270) 266; the softmax first in line, and no maximum taken 255-263 (1050
+// TFLOP/s; the clock falls to 1.9 GHz under this load).  A turn is now 1300 to 1400 cycles
+// of which the products need 1024.  One wave a SIMD with 64 queries: 458.
+//
+// Heads of 64 take 128 registers and half the LDS, so that two workgroups share a unit:
+// 216 -> 175 us at 4 x 4096 tokens, 16 and 4 heads of 64 (157 with the steps above).
 __device__ __forceinline__ void meet() {
   __builtin_amdgcn_sched_barrier(0);
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -273,10 +288,14 @@ __device__ __host__ constexpr size_t split_floats() {
   return (size_t)kSplitRows * (kHd + 2);
 }
 
+// Bound by memory with single queries: keys and values are read once, 32 rows share them.
 // A row of a tile is (query, head of the group): rows of a sequence are numbered
 // query * group + head, so that the heads that share keys share the tile.  Each
 // wave keeps its own two places for keys and two for values in LDS and waits for nobody;
-// the waves' states are joined at the end.
+// the waves' states are joined at the end.  One query over 131071 keys, 16 and 8 heads of
+// 128: 537 MB in 99 us and 6 more for the join (138 us with one tile of read-ahead and one
+// load at a time in the join); 64 queries of 64 sequences over up to 8192 keys with a
+// window of 4096: 988 MB in 175 us, some of it from the last-level cache.
 template <int kHd>
 __global__ void __launch_bounds__(64 * kSplitWaves) attn_split_kernel(AttnArgs a, int splits) {
   constexpr int kTile = kTileBytes<kHd>(kSplitKeys);

@@ -3,13 +3,17 @@
 //
 //   n = x r w,  r = 1 / sqrt(mean(x^2) + eps);  (a', b') = (a c - b s, b c + a s)
 //
-// Everything here is bound by memory: 2 bytes in and 2 out per element (4 in, 2
-// out backward), a handful of operations each.  A team of head_dim / 8 lanes
-// holds one head, 16 bytes a lane, so that a wave reads 4 (or 8) whole heads of
-// one token per load and the norm's sum is three or four DPP adds.  The pairs of
-// the half layout lie rot/2 elements apart: the partner's raw 16 bytes come from
-// the lane rot/16 away by a lane permute, not by a second read.  A token's
-// cosines and sines are loaded once per wave and used for all its heads.
+// Everything here is bound by memory, or by its launch: 2 bytes in and 2 out per element
+// (4 in, 2 out backward), a handful of operations each.  16384 tokens of 24 heads of 128:
+// the norms with the rotation 41 us (5.0 TB/s, the rate of a large copy), their backward
+// 56 us and 4 to sum the weights' gradients (5.0 TB/s); the rotation alone of 16381 tokens
+// of 16 heads 27 us (5.1 TB/s); one token 2.6 us, 32 tokens into a cache 4.5 us.
+//
+// A team of head_dim / 8 lanes holds one head, 16 bytes a lane, so that a wave reads 4 (or
+// 8) whole heads of one token per load and the norm's sum is three or four DPP adds.  The
+// pairs of the half layout lie rot/2 elements apart: the partner's raw 16 bytes come from
+// the lane rot/16 away by a lane permute, not by a second read.  A token's cosines and
+// sines are loaded once per wave and used for all its heads.
 #include "device_common.h"
 #include "launch_attention.h"
 
@@ -199,9 +203,12 @@ hipError_t launch_rope(const RopeArgs &a, hipStream_t stream) {
   constexpr int kTeams = 64 / (kHd / 8);
   const int heads = a.heads_q + a.heads_k + a.heads_v;
   const int groups = (heads + kTeams - 1) / kTeams;
-  // Two waves a token (three batched loads of 4 heads each for 24 heads); with few
-  // tokens one wave per group of heads, so that no wave loops.
-  int parts = a.tokens >= 1024 ? 2 : groups;
+  // Waves a token: one where the tokens alone fill the card, one per group of heads where
+  // they are few, so that no wave loops.  Norms of 24 heads of 128, back to back in a graph,
+  // 1 / 2 / 3 / 6 waves, us: 32 tokens 4.7 / 3.5 / 3.2 / 3.0; 512 tokens 5.2 / 4.0 / 4.1 /
+  // 4.2; 2048 tokens 8.4 / 8.1 / 7.9 / 9.5; 4096 tokens 11.4 / 12.6 / 12.9 / 15.6; 16384
+  // tokens 37.1 / 38.6 / 42.7 / 60.5.
+  int parts = a.tokens >= 4096 ? 1 : a.tokens >= 512 ? 2 : groups;
   if (parts > groups) parts = groups;
   const int64_t blocks = (a.tokens * parts + kWaves - 1) / kWaves;
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
