@@ -161,15 +161,17 @@ __global__ void __launch_bounds__(64 * kDqWaves, kHd == 64 ? 4 : 2) attn_dq_kern
 #pragma unroll
       for (int kk = 0; kk < kHd / 16; ++kk) s = mfma(row_frag<kHd>(ktile, 32 * b, kk), qf[kk], s);
       copy(i + 1, b * kParts / 2);
+      feed<2, kHd / 16, 0>();
+      // Masked here, so that the exponentials run beside do v: 832 -> 826 us (4 x 4096 tokens).
+      if (!all) mask_tile(s, key0 + 32 * b, p, a.window, a.sinks);
 #pragma unroll
       for (int kk = 0; kk < kHd / 16; ++kk) dp = mfma(row_frag<kHd>(vtile, 32 * b, kk), df[kk], dp);
       if (kParts == 4) copy(i + 1, b * 2 + 1);
-      feed<2, kHd / 8, 0>();
-      if (!all) mask_tile(s, key0 + 32 * b, p, a.window, a.sinks);
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        s[j] = kKept ? __builtin_amdgcn_exp2f(s[j] * c2) * dp[j]
-                     : __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], c2, sd * c2)) * (dp[j] - dd);
+      for (int j = 0; j < 16; ++j) s[j] = __builtin_amdgcn_exp2f(kKept ? s[j] * c2 : __builtin_fmaf(s[j], c2, sd * c2));
+      feed<2, kHd / 16, 0>();
+#pragma unroll
+      for (int j = 0; j < 16; ++j) s[j] *= kKept ? dp[j] : dp[j] - dd;
 #pragma unroll
       for (int step = 0; step < 2; ++step) {
         const bf16x8 sf = pack_step(s, step);
@@ -200,7 +202,8 @@ constexpr int kDkWaves = 4, kDkRows = 32 * kDkWaves, kDkQueries = 64;
 // two waves a SIMD; the matrix cores are busy 55% of the time (550 GFLOP in 490 us at 4 x
 // 4096 tokens, 16 and 8 heads of 128).  What it took, the whole backward call there, us:
 // 1492 as first built; masks without branches, reads ahead of the products and long walks
-// first 973; copies between the products 903; starting values in the accumulators 863.
+// first 973; copies between the products 903; starting values in the accumulators 863 (826 to
+// 863 from card to card).
 // One wave a SIMD with twice the registers: 1150 where this took 979.
 //
 // Work on one block of 128 keys and one key head: tiles of 64 queries of each head of
@@ -407,17 +410,27 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
 #pragma unroll
       for (int kk = 0; kk < kHd / 16; ++kk) s = mfma(row_frag<kHd>(qtile, 32 * b, kk), kf[kk], s);
       copy(from, buf ^ 1, b * kParts / 2);
-#pragma unroll
-      for (int kk = 0; kk < kHd / 16; ++kk) dp = mfma(row_frag<kHd>(dtile, 32 * b, kk), vf[kk], dp);
-      if (kParts == 4) copy(from, buf ^ 1, b * 2 + 1);
-      feed<2, kHd / 8, 0>();
-      if (!all) {
+      // The mask between the products lets the exponentials run beside the second ones, but
+      // takes registers: uneven sequences, heads of 64: 107 -> 105 us; 4 x 4096 tokens, heads
+      // of 128: 832 -> 838 us.
+      constexpr bool kEarly = kHd == 64;
+      auto mask = [&]() {
+        if (all) return;
         int since = p_lo + 4 * half - seen_lo;
         asm volatile("" : "+v"(since));      // keeps the comparisons inside this branch
 #pragma unroll
         for (int j = 0; j < 16; ++j)
           s[j] = (uint32_t)(since + 8 * (j / 4) + j % 4) < seen_n ? s[j] : -__builtin_inff();
+      };
+      if (kEarly) {
+        feed<2, kHd / 16, 0>();
+        mask();
       }
+#pragma unroll
+      for (int kk = 0; kk < kHd / 16; ++kk) dp = mfma(row_frag<kHd>(dtile, 32 * b, kk), vf[kk], dp);
+      if (kParts == 4) copy(from, buf ^ 1, b * 2 + 1);
+      feed<2, kEarly ? kHd / 16 : kHd / 8, 0>();
+      if (!kEarly) mask();
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         s[j] = __builtin_amdgcn_exp2f(s[j] * c2);
