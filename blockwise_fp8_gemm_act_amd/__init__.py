@@ -3,8 +3,8 @@ blockwise-scaled FP8 GEMM and the attention block for MI355X (gfx950).
 
 Argument marshalling only.  Every step of the computation runs in the HIP
 kernels behind the C ABI declared in ``include/puro.h`` and
-``include/puro_attention.h``; PyTorch is used for device memory and streams.  There is no fallback: if the library is missing,
-importing this package fails.
+``include/puro_attention.h``; PyTorch is used for device memory and streams.
+There is no fallback: if the library is missing, importing this package fails.
 
 The raw C calls keep their C names (``puro_quant_act_1x128``,
 ``puro_quant_w_128x128``, ``puro_quant_transpose``, ``puro_quant_weights``, ``puro_requant_act_t``,

@@ -155,7 +155,8 @@ def rope(x, table, pos=None, layout: str = "half", inverse: bool = False, out=No
     n, h, d = x.shape
     r = _rotation(table, pos, layout, n, d, x.device)
     y, ys = _out(out, "out", (n, h, d), x.device)
-    _puro._check(_lib.puro_rope(r, inverse, x.data_ptr(), xs, n, h, d, y.data_ptr(), ys, _stream(stream, x.device)), "puro_rope")
+    _puro._check(_lib.puro_rope(r, inverse, x.data_ptr(), xs, n, h, d, y.data_ptr(), ys, _stream(stream, x.device)),
+                 "puro_rope")
     return y
 
 

@@ -97,7 +97,8 @@ puro_status norm_rope(const puro_rotation *r, const uint16_t *x, int64_t x_strid
   if (!heads_ok(tokens, q_heads, k_heads, head_dim) || !rotation_shape(r, head_dim)) return PURO_ERR_SHAPE;
   const int64_t v_heads = append ? k_heads : 0, heads = q_heads + k_heads + v_heads;
   const int64_t k_rows = append ? cache_rows : tokens;
-  if (!strided_ok(tokens, heads * head_dim, x_stride) || !strided_ok(tokens, q_heads * head_dim, q_stride)) return PURO_ERR_SHAPE;
+  if (!strided_ok(tokens, heads * head_dim, x_stride) || !strided_ok(tokens, q_heads * head_dim, q_stride))
+    return PURO_ERR_SHAPE;
   if (k_rows < 0 || k_rows > kMaxDim || !strided_ok(k_rows, k_heads * head_dim, k_stride)) return PURO_ERR_SHAPE;
   if (append && !strided_ok(k_rows, k_heads * head_dim, v_stride)) return PURO_ERR_SHAPE;
   if (!(eps > 0.0f) || !std::isfinite(eps)) return PURO_ERR_VALUE;
@@ -210,7 +211,8 @@ puro_status puro_rope(const puro_rotation *r, int inverse, const uint16_t *x, in
                       int64_t heads, int64_t head_dim, uint16_t *y, int64_t y_stride, puro_stream_t stream) {
   if (puro_status s = rotation_mode(r)) return s;
   if (!heads_ok(tokens, heads, 0, head_dim) || !rotation_shape(r, head_dim)) return PURO_ERR_SHAPE;
-  if (!strided_ok(tokens, heads * head_dim, x_stride) || !strided_ok(tokens, heads * head_dim, y_stride)) return PURO_ERR_SHAPE;
+  if (!strided_ok(tokens, heads * head_dim, x_stride) || !strided_ok(tokens, heads * head_dim, y_stride))
+    return PURO_ERR_SHAPE;
   if (tokens == 0 || heads == 0) return PURO_OK;
   if (!r->table || !x || !y) return PURO_ERR_NULL;
   if (!aligned16(r->table) || !aligned16(x) || !aligned16(y) || !aligned4(r->pos)) return PURO_ERR_ALIGN;
@@ -263,7 +265,8 @@ puro_status puro_qk_norm_rope_backward(const puro_rotation *r, const uint16_t *d
   if (!(eps > 0.0f) || !std::isfinite(eps)) return PURO_ERR_VALUE;
   const bool some = tokens > 0 && heads > 0;
   if (!dwq || !dwk) return PURO_ERR_NULL;
-  if (some && (!r->table || !x || !dx || (q_heads > 0 && (!dq || !wq)) || (k_heads > 0 && (!dk || !wk)))) return PURO_ERR_NULL;
+  if (some && (!r->table || !x || !dx || (q_heads > 0 && (!dq || !wq)) || (k_heads > 0 && (!dk || !wk))))
+    return PURO_ERR_NULL;
   if (!aligned16(dq) || !aligned16(dk) || !aligned16(x) || !aligned16(wq) || !aligned16(wk) || !aligned16(dx) ||
       !aligned16(dwq) || !aligned16(dwk) || !aligned16(r->table) || !aligned16(workspace) || !aligned4(r->pos))
     return PURO_ERR_ALIGN;

@@ -500,7 +500,8 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int splits) 
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int s = s0 + e;
-      const float f = s < splits ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(s < 64 ? ms[0] : ms[1]), s & 63)) : 0.0f;
+      const float w = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(s < 64 ? ms[0] : ms[1]), s & 63));
+      const float f = s < splits ? w : 0.0f;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) x[j] += one[e][j] * f;
     }
@@ -581,7 +582,8 @@ AttnPlan plan_attention(const puro_attention_shape &a) {
   p.pack = group % 4 == 0 ? 4 : group % 2 == 0 ? 2 : 1;
   const int tall = kFwdRows / p.pack;
   const double wm = (double)a.sequences * (int64_t)((ql + tall - 1) / tall) * (a.q_heads / p.pack);
-  const double t_many = (wm < units ? 1 : wm / units) * (start_many + per_many * (wm < units ? most(tall) : mean(tall)) / kFwdKeys);
+  const double walk_many = wm < units ? most(tall) : mean(tall);
+  const double t_many = (wm < units ? 1 : wm / units) * (start_many + per_many * walk_many / kFwdKeys);
 
   p.split = t_few < t_many;
   p.splits = 1;

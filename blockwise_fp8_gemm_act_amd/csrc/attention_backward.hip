@@ -597,12 +597,14 @@ hipError_t launch(const AttnArgs &a, hipStream_t stream) {
   }
   if (a.k_tokens == 0) return hipSuccess;
   const DkPlan plan = plan_dk(a.q_tokens, a.k_tokens, a.sequences, a.q_heads, a.k_heads, kHd, a.window, a.sinks);
-  const int64_t items = (int64_t)plan.far_slots * plan.far_blocks + (int64_t)Order(plan.slots, a.sequences, a.window).count() * plan.parts;
+  const int64_t near = (int64_t)Order(plan.slots, a.sequences, a.window).count() * plan.parts;
+  const int64_t items = (int64_t)plan.far_slots * plan.far_blocks + near;
   attn_dkdv_kernel<kHd><<<dim3((unsigned)(items * a.k_heads)), dim3(64 * kDkWaves), 0, stream>>>(a, plan);
   if (hipError_t e = hipGetLastError()) return e;
   if (plan.parts > 1 || plan.far_blocks > 0) {
     const int chunks = kDkRows / (256 / (kHd / 8));
-    attn_dkdv_join_kernel<kHd><<<dim3((unsigned)((int64_t)plan.slots * chunks * a.k_heads)), dim3(256), 0, stream>>>(a, plan);
+    const int64_t blocks = (int64_t)plan.slots * chunks * a.k_heads;
+    attn_dkdv_join_kernel<kHd><<<dim3((unsigned)blocks), dim3(256), 0, stream>>>(a, plan);
     return hipGetLastError();
   }
   return hipSuccess;

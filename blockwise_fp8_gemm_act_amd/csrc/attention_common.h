@@ -107,7 +107,8 @@ __device__ __forceinline__ Seq find_seq(const AttnArgs &a, const int32_t *start,
 // is even, and neighbours in the sequence share keys: as numbered.
 struct Order {
   int slots, parts;
-  __device__ __host__ __forceinline__ Order(int slots, int sequences, int window) : slots(slots), parts(window > 0 ? 1 : sequences) {}
+  __device__ __host__ __forceinline__ Order(int slots, int sequences, int window)
+      : slots(slots), parts(window > 0 ? 1 : sequences) {}
   __device__ __host__ __forceinline__ int each() const { return (slots + parts - 1) / parts; }
   __device__ __host__ __forceinline__ int count() const { return each() * parts; }
   __device__ __forceinline__ int operator()(int x) const { return x % parts * each() + x / parts; }
