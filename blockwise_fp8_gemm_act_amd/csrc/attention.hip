@@ -83,9 +83,9 @@ constexpr int kFwdRows = 32 * kFwdWaves;
 // freely 342; turns 289; copies spread between the products (together they stall their
 // wave as long as the softmax) and heads that share keys in one block 278; addresses of
 // the copies worked out a turn ahead (a turn's products issue 200 other instructions
-// instead of 270) 266; the softmax first in line, and no maximum taken 255-263 (1050
-// TFLOP/s; the clock falls to 1.9 GHz under this load).  A turn is now 1300 to 1400 cycles
-// of which the products need 1024.  One wave a SIMD with 64 queries: 458.
+// instead of 270) 266; the softmax first in line, and no maximum taken 248 to 262 from card
+// to card (1050 to 1110 TFLOP/s; the clock falls to 1.9 GHz under this load).  A turn is now
+// 1300 to 1400 cycles of which the products need 1024.  One wave a SIMD with 64 queries: 458.
 //
 // Heads of 64 take 128 registers and half the LDS, so that two workgroups share a unit:
 // 216 -> 175 us at 4 x 4096 tokens, 16 and 4 heads of 64 (157 with the steps above).

@@ -24,8 +24,8 @@ __device__ __forceinline__ f32x16 splat(float x) {
 // ---------------------------------------------------------------- dq
 constexpr int kDqWaves = 4, kDqRows = 32 * kDqWaves, kDqKeys = 64;
 
-// Three products a pair (S, do v, dS k): bound by the matrix cores, busy 60% of the time
-// (counters, 4 x 4096 tokens, 16 and 8 heads of 128: 412 GFLOP in 355 us).  Two workgroups
+// Three products a pair (S, do v, dS k): bound by the matrix cores, busy 61% of the time
+// (counters, 4 x 4096 tokens, 16 and 8 heads of 128: 412 GFLOP in 352 us).  Two workgroups
 // a unit at heads of 128, whose waves fill each other's gaps; of heads of 64 four.
 //
 // A workgroup takes `pack` heads of a group by kDqRows / pack queries, as the forward
@@ -199,12 +199,11 @@ constexpr int kDkWaves = 4, kDkRows = 32 * kDkWaves, kDkQueries = 64;
 // Four products a pair (S, do v, P^T do, dS^T q).  Keys stand as columns here, so that a
 // lane owns a key, and P and dS are again operands in place.  A wave holds 32 keys and
 // values (64 registers at heads of 128) and the sums of their gradients (128), which leaves
-// two waves a SIMD; the matrix cores are busy 55% of the time (550 GFLOP in 490 us at 4 x
+// two waves a SIMD; the matrix cores are busy 57% of the time (550 GFLOP in 476 us at 4 x
 // 4096 tokens, 16 and 8 heads of 128).  What it took, the whole backward call there, us:
 // 1492 as first built; masks without branches, reads ahead of the products and long walks
-// first 973; copies between the products 903; starting values in the accumulators 863 (826 to
-// 863 from card to card).
-// One wave a SIMD with twice the registers: 1150 where this took 979.
+// first 973; copies between the products 903; starting values in the accumulators 823 to 863
+// from card to card.  One wave a SIMD with twice the registers: 1150 where this took 979.
 //
 // Work on one block of 128 keys and one key head: tiles of 64 queries of each head of
 // the group.  `near` tiles hold the queries that have the block in their window; for a
