@@ -172,7 +172,7 @@ def test_attention():
     for change in BAD_SHAPES:
         assert f(shape(**change)) == SHAPE, change
         assert puro.puro_attention_workspace_bytes(shape(**change)) == 0
-    for scale in (0.0, -1.0, float("inf"), float("nan")):
+    for scale in (0.0, -1.0, 1e-31, float("inf"), float("nan")):
         assert f(shape(scale=scale)) == VALUE
     assert f(shape(q_tokens=0), q=None, o=None) == OK
     for change in (dict(q=None), dict(k=None), dict(v=None), dict(o=None), dict(qst=None), dict(kst=None), dict(qst=None, kst=None)):
