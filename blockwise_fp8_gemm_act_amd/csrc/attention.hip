@@ -386,11 +386,18 @@ __global__ void __launch_bounds__(64 * kSplitWaves) attn_split_kernel(AttnArgs a
     younger(two);
 #pragma unroll
     for (int step = 0; step < 2; ++step) {
-      const bf16x8 pf = pack_step(s, step);
+      // P in two parts, so that its rounding adds nothing to the output's own (relative error
+      // 0.0016 instead of 0.0023).  Where memory is the bound, the matrix cores have time for
+      // it (single tokens: unchanged; 1 x 512 queries over 16896 keys: 192 -> 209 us).
+      const bf16x8 pf = pack_step(s, step), pr = pack_rest(s, step, pf);
 #pragma unroll
-      for (int d = 0; d < kHd / 32; ++d) st.o[d] = mfma(col_frag<kHd>(vtile, 16 * step, d), pf, st.o[d]);
+      for (int d = 0; d < kHd / 32; ++d) {
+        const bf16x8 v = col_frag<kHd>(vtile, 16 * step, d);
+        st.o[d] = mfma(v, pf, st.o[d]);
+        st.o[d] = mfma(v, pr, st.o[d]);
+      }
     }
-    feed<4, 0, kHd / 16>();
+    feed<4, 0, kHd / 16, 2>();
     if (two) {
       read();
       copy_values(i + 2 * kSplitWaves, odd);
@@ -541,9 +548,9 @@ hipError_t launch(const AttnArgs &a, const AttnPlan &plan, hipStream_t stream) {
 // run at a time; the constants, in us, are fitted to 47 shapes of heads of 128 and 97 of
 // heads of 64, with 1 to 64 sequences, 8 to 4096 queries and up to 16384 earlier keys (97
 // shapes: on average 0.3% slower than the better kernel, 17% at worst).  Examples (many /
-// few queries' kernel), 16 and 8 heads of 128: 64 x 8 queries over 2056 keys 266 / 124 us;
-// 16 x 64 over 2112 67 / 61; 8 x 512 over 512 34 / 66; 1 x 4096 over 4096 113 / 229;
-// 1 x 512 over 16896 755 / 192.
+// few queries' kernel), 16 and 8 heads of 128: 64 x 8 queries over 2056 keys 266 / 127 us;
+// 16 x 64 over 2112 67 / 63; 8 x 512 over 512 34 / 66; 1 x 4096 over 4096 113 / 229;
+// 1 x 512 over 16896 755 / 209.
 AttnPlan plan_attention(const puro_attention_shape &a) {
   AttnPlan p{};
   const double units = 256.0;

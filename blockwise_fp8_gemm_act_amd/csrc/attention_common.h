@@ -291,13 +291,14 @@ __device__ __forceinline__ bf16x8 col_frag(uint32_t tile, int r0, int db) {
 // Order of a block of products: the LDS reads of the first `ahead` products go out
 // first, then each product is followed by the reads of one further on (one a product
 // of row fragments, two of column fragments; `rows` products of the first kind come
-// first).  Left alone, the compiler reads, waits and multiplies one by one.
-template <int kAhead, int kRowProducts, int kColProducts>
+// first).  kTimes: products of each fragment.  Left alone, the compiler reads, waits and
+// multiplies one by one.
+template <int kAhead, int kRowProducts, int kColProducts, int kTimes = 1>
 __device__ __forceinline__ void feed() {
   constexpr int n = kRowProducts + kColProducts;
 #pragma unroll
   for (int j = 0; j < n + kAhead; ++j) {
-    if (j >= kAhead) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if (j >= kAhead) __builtin_amdgcn_sched_group_barrier(0x008, kTimes, 0);
     if (j < n) {
       if (j < kRowProducts) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       else __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
@@ -310,6 +311,16 @@ __device__ __forceinline__ bf16x8 pack_step(const f32x16 &p, int s) {
   u32x4 w;
 #pragma unroll
   for (int j = 0; j < 4; ++j) w[j] = pack_bf16(p[8 * s + 2 * j], p[8 * s + 2 * j + 1]);
+  return __builtin_bit_cast(bf16x8, w);
+}
+
+// And what their rounding left out, in the same place.
+__device__ __forceinline__ bf16x8 pack_rest(const f32x16 &p, int s, bf16x8 rounded) {
+  const u32x4 r = __builtin_bit_cast(u32x4, rounded);
+  u32x4 w;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    w[j] = pack_bf16(p[8 * s + 2 * j] - __uint_as_float(r[j] << 16), p[8 * s + 2 * j + 1] - __uint_as_float(r[j] & 0xffff0000u));
   return __builtin_bit_cast(bf16x8, w);
 }
 

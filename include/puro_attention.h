@@ -184,7 +184,8 @@ size_t puro_attention_backward_workspace_bytes(const puro_attention_shape *a);
  *   o    [q_tokens][q_heads][head_dim] bf16, o_stride (output)
  *   lse  [q_heads][q_tokens] fp32 (output), or NULL
  * Products are bf16 with fp32 sums; exp(S - running maximum) is rounded to bf16
- * for its product with v, its sum is not.  Deterministic for a given shape.
+ * (for few queries to two of them, 16 bits) for its product with v, its sum is
+ * not.  Deterministic for a given shape.
  */
 puro_status puro_attention(const puro_attention_shape *a, const uint16_t *q, const uint16_t *k, const uint16_t *v,
                            const int32_t *q_start, const int32_t *k_start, const int32_t *k_len, uint16_t *o,
