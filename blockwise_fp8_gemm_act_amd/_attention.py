@@ -216,25 +216,29 @@ def qk_norm_rope_backward(dq, dk, x, wq, wk, table, pos=None, *, eps: float = 1e
     pq, pk = _weight(wq, "wq", d, dev), _weight(wk, "wk", d, dev)
     dx, dxs = _out(dx, "dx", (n, qh + kh, d), dev)
     dw = _puro.empty((2, d), dtype=torch.float32, device=dev)
-    workspace, size = _workspace(workspace, _lib.puro_qk_norm_rope_backward_workspace_bytes(n, d), dev)
+    ws = _workspace(workspace, _lib.puro_qk_norm_rope_backward_workspace_bytes(n, d), dev)
     _puro._check(_lib.puro_qk_norm_rope_backward(r, dq.data_ptr(), dqs, dk.data_ptr(), dks, x.data_ptr(), xs, n, qh, kh,
                                                  d, pq, pk, eps, dx.data_ptr(), dxs, dw.data_ptr(),
-                                                 dw.data_ptr() + 4 * d, workspace, size, _stream(stream, dev)),
+                                                 dw.data_ptr() + 4 * d, *_span(ws), _stream(stream, dev)),
                  "puro_qk_norm_rope_backward")
     return dx, dw[0], dw[1]
 
 
 # ---------------------------------------------------------------- attention
 def _workspace(ws, need, device):
-    """(pointer, bytes) of the caller's workspace, or of a new one where one is needed.  The caching allocator keeps
-    a released workspace on its stream, where the kernels that use it are already enqueued."""
+    """The caller's workspace, or a new one where one is needed, else None.  The call holds the tensor until it has
+    enqueued its kernels: only then is a released block's memory safe, as the caching allocator gives it to later work
+    of the same stream."""
     if ws is None:
-        if need == 0:
-            return None, 0
-        ws = _puro.empty((need,), dtype=torch.uint8, device=device)
-    elif not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous() or ws.device != device:
+        return _puro.empty((need,), dtype=torch.uint8, device=device) if need else None
+    if not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous() or ws.device != device:
         raise ValueError("workspace must be a contiguous CUDA tensor on %s" % device)
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    return ws
+
+
+def _span(ws):
+    """(pointer, bytes) of a workspace."""
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
 
 
 def _attention_shape(q, k, v, q_start, k_start, k_len, window, sinks, scale, max_k):
@@ -271,9 +275,9 @@ def attention(q, k, v, q_start=None, k_start=None, k_len=None, *, window: int = 
     a, pqs, pks, pkl = _attention_shape(q, k, v, q_start, k_start, k_len, window, sinks, scale, max_k)
     o, a.o_stride = _out(out, "out", tuple(q.shape), q.device)
     lse = _puro.empty((a.q_heads, a.q_tokens), dtype=torch.float32, device=q.device)
-    ws, size = _workspace(workspace, _lib.puro_attention_workspace_bytes(a), q.device)
+    ws = _workspace(workspace, _lib.puro_attention_workspace_bytes(a), q.device)
     _puro._check(_lib.puro_attention(a, q.data_ptr(), k.data_ptr(), v.data_ptr(), pqs, pks, pkl, o.data_ptr(),
-                                     lse.data_ptr(), ws, size, _stream(stream, q.device)), "puro_attention")
+                                     lse.data_ptr(), *_span(ws), _stream(stream, q.device)), "puro_attention")
     return o, lse
 
 
@@ -292,8 +296,8 @@ def attention_backward(do, q, k, v, o, lse, q_start=None, k_start=None, *, windo
     dq, a.dq_stride = _out(dq, "dq", tuple(q.shape), dev)
     dk, a.dk_stride = _out(dk, "dk", tuple(k.shape), dev)
     dv, a.dv_stride = _out(dv, "dv", tuple(v.shape), dev)
-    ws, size = _workspace(workspace, _lib.puro_attention_backward_workspace_bytes(a), dev)
+    ws = _workspace(workspace, _lib.puro_attention_backward_workspace_bytes(a), dev)
     _puro._check(_lib.puro_attention_backward(a, do.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                                              lse.data_ptr(), pqs, pks, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws,
-                                              size, _stream(stream, dev)), "puro_attention_backward")
+                                              lse.data_ptr(), pqs, pks, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                              *_span(ws), _stream(stream, dev)), "puro_attention_backward")
     return dq, dk, dv
