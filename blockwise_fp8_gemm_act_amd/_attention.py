@@ -79,7 +79,7 @@ def _heads_tensor(t, name, heads=None, head_dim=None, tokens=None, device=None):
     s, sh, sd = t.stride()
     if (d > 1 and sd != 1) or (h > 1 and sh != d):
         raise ValueError("%s must have densely packed heads" % name)
-    return s if n > 1 else -(-(max(s, h * d)) // 8) * 8
+    return s if n > 1 else -(-h * d // 8) * 8          # one token's stride means nothing
 
 
 def _ints(t, name, n, device):
@@ -118,7 +118,7 @@ def _rows2d(x, name, width):
         raise ValueError("%s needs at least %d columns, got %d" % (name, width, x.shape[1]))
     if x.shape[1] > 1 and x.stride(1) != 1:
         raise ValueError("%s must have contiguous rows" % name)
-    return x.stride(0) if x.shape[0] > 1 else -(-(max(x.stride(0), width)) // 8) * 8
+    return x.stride(0) if x.shape[0] > 1 else -(-width // 8) * 8
 
 
 def _out(t, name, shape, device):

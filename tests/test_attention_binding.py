@@ -86,3 +86,32 @@ def test_the_callers_workspace_is_passed(library, call):
     assert library.calls[-1][1][-3:-1] == (ws.data_ptr(), 3 * NEED)
     with pytest.raises(ValueError):
         call(workspace=torch.zeros(NEED, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("tokens", [0, 1])
+def test_one_tokens_strides_mean_nothing(library, tokens):
+    """Slices of rows of any length, also past the longest distance between tokens, where there is no second token."""
+    def part(heads, at, width):
+        return torch.zeros(at + heads * 64, dtype=torch.bfloat16)[at:].as_strided((tokens, heads, 64), (width, 64, 1)).as_subclass(Cuda)
+
+    q, k, v, o, do = part(4, 8, 512), part(2, 16, 1 << 24), part(2, 24, 7), part(4, 0, 256), part(4, 32, 1 << 30)
+    lse = fake((4, tokens), torch.float32)
+    puro.attention(q, k, v, out=o)
+    puro.attention_backward(do, q, k, v, o, lse)
+    assert [n for n, _ in library.calls] == ["puro_attention", "puro_attention_backward"]
+    for _, args in library.calls:
+        a = args[0]
+        assert (a.q_stride, a.k_stride, a.v_stride, a.o_stride) == (256, 128, 128, 256)
+    x = torch.zeros(512, dtype=torch.bfloat16).as_strided((tokens, 512), (1 << 25, 1)).as_subclass(Cuda)
+    w, table = fake((64,)), fake((8, 2, 32), torch.float32)
+    puro.qk_norm_rope(x, w, w, table, q_heads=4, k_heads=2)
+    assert library.calls[-1][1][2] == 384
+
+
+def test_several_tokens_keep_their_strides(library):
+    q, kv, lse = fake((5, 6, 64))[:, 1:5], fake((9, 2, 64)), fake((4, 5), torch.float32)
+    puro.attention_backward(q, q, kv, kv, q, lse)
+    a = library.calls[-1][1][0]
+    assert (a.q_stride, a.k_stride, a.o_stride, a.dq_stride) == (384, 128, 384, 256)
+    with pytest.raises(ValueError):
+        puro.attention_backward(fake((5, 4, 64)), q, kv, kv, q, lse)
