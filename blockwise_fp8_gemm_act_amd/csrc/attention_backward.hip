@@ -7,6 +7,8 @@
 // and a fixed order: no atomics, and no fp32 copy of dq in memory.
 #include "attention_common.h"
 
+#include <type_traits>
+
 namespace puro {
 namespace {
 
@@ -36,6 +38,7 @@ template <int kHd>
 __global__ void __launch_bounds__(64 * kDqWaves, kHd == 64 ? 4 : 2) attn_dq_kernel(AttnArgs a, int slots, int pack) {
   constexpr int kTile = kTileBytes<kHd>(kDqKeys);
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2][2][kTile];
+  __shared__ int again[kDqWaves];
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int hk = (int)(blockIdx.x % a.k_heads);
@@ -93,11 +96,22 @@ __global__ void __launch_bounds__(64 * kDqWaves, kHd == 64 ? 4 : 2) attn_dq_kern
   arrived(df);
   const float c2 = a.scale * kLog2e;
 
-  // D = do.o carries the rounding of o to bf16.  Over n visible keys that is a 1/sqrt(n)
-  // part of dS's own rounding, but where a row sees a handful of keys it is all there is:
-  // with one key dS is 0.  Blocks with such rows first correct D by the sum of their dS,
-  // which is 0 for the exact D.
+  // D = do.o carries the rounding of o to bf16, up to 2^-8 |do| |o|, which no other rounding
+  // hides where dS is small against D: rows with a dominating key, values or keys with a mean.
+  // With the exact D a row's dS sum to 0, so that their sum is D's error; the stats below always
+  // have it put right.  In dq it adds (sum dS) (sum P k), beside roundings of dS that come to
+  // 2^-9 of the root of the squared dS times |k|.  Waves with a row whose sum reaches 2^-6 of
+  // that root walk their keys again with the D put right.  Mean relative error of dq's rows (the
+  // worst row's), 4096 keys, before / so / with the exact D: independent inputs 0.0017 / 0.0017 /
+  // 0.0017; keys and values with a mean of three deviations 0.51 (2.3) / 0.006 (0.05) / 0.005
+  // (0.02); a key that takes nearly all 1.1 (43) / 0.0016 (0.015) / 0.0015 (0.004).  The sums
+  // cost 2% and a walk again in every block 40% of the backward call (4 x 4096 tokens: 842 us
+  // without, 861 with the sums, 873 with the few walks of that case, 1176 with all); a bound of
+  // 2^-7 instead takes 918.  Blocks of rows with few keys nearly always need it: they take D
+  // from a walk of its own first, two products instead of three.
+  bool exact = false;
   if (kt.count > 0 && (shift + row0 < 128 || (a.window > 0 && a.window + a.sinks < 128))) {
+    exact = true;
     float off = 0.0f;
     for (int i = 0; i < kt.count; ++i) {
       wait_all_and_meet();
@@ -119,73 +133,102 @@ __global__ void __launch_bounds__(64 * kDqWaves, kHd == 64 ? 4 : 2) attn_dq_kern
     wait_all_and_meet();
     copy_all(0);
   }
-  if (half == 0 && mine < rows) {
-    a.ws[(int64_t)h * a.q_tokens + qrow] = sd;
-    a.ws[(int64_t)(a.q_heads + h) * a.q_tokens + qrow] = -dd;
-  }
 
   // Starting values kept in registers, where there are enough of them.
   constexpr bool kKept = kHd == 128;
-  f32x16 s0, dp0;
-  if (kKept) {
-    s0 = splat(sd);
-    dp0 = splat(-dd);
-    asm volatile("" : "+v"(s0), "+v"(dp0));
-  }
   f32x16 acc[kHd / 32];
 #pragma unroll
   for (int d = 0; d < kHd / 32; ++d) acc[d] = (f32x16){};
   // Tiles that this wave's queries see; the others are only copied for the rest.
   const int before = a.window > 0 ? w_lo - a.window + 1 : 0;            // first key in the wave's window
   const bool firsts = kt.first_n > 0 || kt.main0 * kDqKeys < a.sinks;   // the first tiles hold first keys
-  const int on = firsts || before <= 0 ? 0 : clampi(before / kDqKeys - kt.main0, 0, kt.count);
+  int on = firsts || before <= 0 ? 0 : clampi(before / kDqKeys - kt.main0, 0, kt.count);
   int seen = kt.count;
   while (seen > on && kt.key0(seen - 1, kDqKeys) > w_hi) --seen;
-  int i = 0;
-  for (; i < on; ++i) {
-    wait_all_and_meet();
-    copy_all(i + 1);
-  }
-  for (; i < seen; ++i) {
-    wait_all_and_meet();
-    const int key0 = kt.key0(i, kDqKeys);
-    const uint32_t ktile = lds0 + (uint32_t)((i & 1) * 2 * kTile), vtile = ktile + kTile;
-    const bool all = key0 + kDqKeys - 1 <= w_lo && (a.window == 0 || key0 > w_hi - a.window);
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      f32x16 s = {}, dp = {};
-      if (kKept) {
-        s = s0;
-        dp = dp0;
-      }
-#pragma unroll
-      for (int kk = 0; kk < kHd / 16; ++kk) s = mfma(row_frag<kHd>(ktile, 32 * b, kk), qf[kk], s);
-      copy(i + 1, b * kParts / 2);
-      feed<2, kHd / 16, 0>();
-      // Masked here, so that the exponentials run beside do v: 832 -> 826 us (4 x 4096 tokens).
-      if (!all) mask_tile(s, key0 + 32 * b, p, a.window, a.sinks);
-#pragma unroll
-      for (int kk = 0; kk < kHd / 16; ++kk) dp = mfma(row_frag<kHd>(vtile, 32 * b, kk), df[kk], dp);
-      if (kParts == 4) copy(i + 1, b * 2 + 1);
-#pragma unroll
-      for (int j = 0; j < 16; ++j) s[j] = __builtin_amdgcn_exp2f(kKept ? s[j] * c2 : __builtin_fmaf(s[j], c2, sd * c2));
-      feed<2, kHd / 16, 0>();
-#pragma unroll
-      for (int j = 0; j < 16; ++j) s[j] *= kKept ? dp[j] : dp[j] - dd;
-#pragma unroll
-      for (int step = 0; step < 2; ++step) {
-        const bf16x8 sf = pack_step(s, step);
-#pragma unroll
-        for (int d = 0; d < kHd / 32; ++d) acc[d] = mfma(col_frag<kHd>(ktile, 32 * b + 16 * step, d), sf, acc[d]);
-      }
-      feed<2, 0, kHd / 16>();
+  // The walk; with kSums also the sum of its dS and of their squares.
+  float off = 0.0f, square = 0.0f;
+  auto walk = [&](auto sums) {
+    constexpr bool kSums = decltype(sums)::value;
+    f32x16 s0, dp0;
+    if (kKept) {
+      s0 = splat(sd);
+      dp0 = splat(-dd);
+      asm volatile("" : "+v"(s0), "+v"(dp0));
     }
-  }
-  for (; i < kt.count; ++i) {
+    if (on < seen) {
+#pragma unroll
+      for (int d = 0; d < kHd / 32; ++d) acc[d] = (f32x16){};
+    }
+    int i = 0;
+    for (; i < on; ++i) {
+      wait_all_and_meet();
+      copy_all(i + 1);
+    }
+    for (; i < seen; ++i) {
+      wait_all_and_meet();
+      const int key0 = kt.key0(i, kDqKeys);
+      const uint32_t ktile = lds0 + (uint32_t)((i & 1) * 2 * kTile), vtile = ktile + kTile;
+      const bool all = key0 + kDqKeys - 1 <= w_lo && (a.window == 0 || key0 > w_hi - a.window);
+      // Unrolled, heads of 64 would keep LDS addresses in scratch (4 x 2048 tokens: 183 -> 188 us).
+#pragma unroll kHd == 64 ? 1 : 2
+      for (int b = 0; b < 2; ++b) {
+        f32x16 s = {}, dp = {};
+        if (kKept) {
+          s = s0;
+          dp = dp0;
+        }
+#pragma unroll
+        for (int kk = 0; kk < kHd / 16; ++kk) s = mfma(row_frag<kHd>(ktile, 32 * b, kk), qf[kk], s);
+        copy(i + 1, b * kParts / 2);
+        feed<2, kHd / 16, 0>();
+        // Masked here, so that the exponentials run beside do v: 832 -> 826 us (4 x 4096 tokens).
+        if (!all) mask_tile(s, key0 + 32 * b, p, a.window, a.sinks);
+#pragma unroll
+        for (int kk = 0; kk < kHd / 16; ++kk) dp = mfma(row_frag<kHd>(vtile, 32 * b, kk), df[kk], dp);
+        if (kParts == 4) copy(i + 1, b * 2 + 1);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) s[j] = __builtin_amdgcn_exp2f(kKept ? s[j] * c2 : __builtin_fmaf(s[j], c2, sd * c2));
+        feed<2, kHd / 16, 0>();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          s[j] *= kKept ? dp[j] : dp[j] - dd;
+          if (kSums) {
+            off += s[j];
+            square = __builtin_fmaf(s[j], s[j], square);
+          }
+        }
+#pragma unroll
+        for (int step = 0; step < 2; ++step) {
+          const bf16x8 sf = pack_step(s, step);
+#pragma unroll
+          for (int d = 0; d < kHd / 32; ++d) acc[d] = mfma(col_frag<kHd>(ktile, 32 * b + 16 * step, d), sf, acc[d]);
+        }
+        feed<2, 0, kHd / 16>();
+      }
+    }
+    for (; i < kt.count; ++i) {
+      wait_all_and_meet();
+      copy_all(i + 1);
+    }
+  };
+  if (!exact) {
+    walk(std::true_type());
+    off = half_sum(off);
+    square = half_sum(square);
+    const bool shows = __any(mine < rows && off != 0.0f && off * off >= 0x1p-12f * square);     // also where both underflow
+    if (__builtin_isfinite(off)) dd += off;
+    again[wave] = shows;
     wait_all_and_meet();
-    copy_all(i + 1);
+    exact = __builtin_amdgcn_readfirstlane(again[0] | again[1] | again[2] | again[3]);
+    if (exact) copy_all(0);
+    if (!shows) on = seen = kt.count;       // this wave only copies for the others
   }
+  if (exact) walk(std::false_type());
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // no copy outlives its workgroup's LDS
+  if (half == 0 && mine < rows) {
+    a.ws[(int64_t)h * a.q_tokens + qrow] = sd;
+    a.ws[(int64_t)(a.q_heads + h) * a.q_tokens + qrow] = -dd;
+  }
   if (mine < rows) {
     uint16_t *out = a.dq + (int64_t)qrow * a.dqs + (int64_t)h * kHd;
 #pragma unroll
