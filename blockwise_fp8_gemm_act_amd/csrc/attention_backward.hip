@@ -95,6 +95,15 @@ __global__ void __launch_bounds__(64 * kDqWaves, kHd == 64 ? 4 : 2) attn_dq_kern
   arrived(qf);
   arrived(df);
   const float c2 = a.scale * kLog2e;
+  if (__any(lse == -__builtin_inff())) {      // rows that see nothing have no part, whatever they hold
+    const bool sees = lse != -__builtin_inff();
+#pragma unroll
+    for (int kk = 0; kk < kHd / 16; ++kk) {
+      qf[kk] = sees ? qf[kk] : (bf16x8){};
+      df[kk] = sees ? df[kk] : (bf16x8){};
+    }
+    dd = sees ? dd : 0.0f;
+  }
 
   // D = do.o carries the rounding of o to bf16, up to 2^-8 |do| |o|, which no other rounding
   // hides where dS is small against D: rows with a dominating key, values or keys with a mean.
@@ -386,23 +395,23 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
   };
   struct Source {
     const uint16_t *q, *d;
-    int last;           // of the tile's rows in the sequence: those past it read it
+    int first, last;    // of the tile's rows in the walk: those outside read one of these (they are masked)
   };
   auto source = [&](Tile x) {
     const int q0 = (tile0 + x.t) * kDkQueries;
     return Source{a.q + (int64_t)(sq.q0 + q0) * a.qs + (int64_t)x.h * kHd,
-                  a.d_o + (int64_t)(sq.q0 + q0) * a.os + (int64_t)x.h * kHd, sq.ql - 1 - q0};
+                  a.d_o + (int64_t)(sq.q0 + q0) * a.os + (int64_t)x.h * kHd, walk.q_lo - q0, walk.q_hi - q0};
   };
   auto copy = [&](const Source &from, int buf, int part) {
     const uint32_t at = lds0 + (uint32_t)(buf * 2 * kTile);
     const int g = part * kDkWaves + wave, r = g * kGroupRows<kHd> + copy_r;
-    const uint32_t in = (uint32_t)(r < from.last ? r : from.last);
+    const uint32_t in = (uint32_t)clampi(r, from.first, from.last);
     dma16_s(from.q, __umul24(in, (uint32_t)(a.qs * 2)) + copy_c * 16, at + (uint32_t)(g * kGroupBytes));
     dma16_s(from.d, __umul24(in, (uint32_t)(a.os * 2)) + copy_c * 16, at + kTile + (uint32_t)(g * kGroupBytes));
   };
-  auto copy_stat = [&](Tile x, int last, int buf) {      // waves 2 and 3 copy what waves 0 and 1 do
+  auto copy_stat = [&](Tile x, const Source &from, int buf) {      // waves 2 and 3 copy what waves 0 and 1 do
     dma4_s(a.ws + (int64_t)((wave & 1) * a.q_heads + x.h) * a.q_tokens + sq.q0 + (tile0 + x.t) * kDkQueries,
-           (uint32_t)((lane < last ? lane : last) * 4), stat0 + (uint32_t)((buf * 2 + (wave & 1)) * kDkQueries * 4));
+           (uint32_t)(clampi(lane, from.first, from.last) * 4), stat0 + (uint32_t)((buf * 2 + (wave & 1)) * kDkQueries * 4));
   };
 
   Tile now{};
@@ -411,7 +420,7 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
     const Source from = source(now);
 #pragma unroll
     for (int part = 0; part < kParts; ++part) copy(from, 0, part);
-    copy_stat(now, from.last, 0);
+    copy_stat(now, from, 0);
   }
   bf16x8 kf[kHd / 16], vf[kHd / 16];
 #pragma unroll
@@ -500,7 +509,7 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
         wait_all_and_meet();
         const Tile next = i + 1 < end ? after(now) : now;
         const Source from = source(next);
-        copy_stat(next, from.last, buf ^ 1);
+        copy_stat(next, from, buf ^ 1);
         return from;
       };
       auto done = [&]() {

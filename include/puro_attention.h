@@ -152,8 +152,9 @@ puro_status puro_qk_norm_rope_backward(const puro_rotation *r, const uint16_t *d
  * Mask.  The queries of a sequence are its last positions: query i of ql
  * queries and kl keys stands at p = kl - ql + i and sees key j when
  *   j <= p  and  (window == 0  or  j > p - window  or  j < sinks).
- * Keys that no query sees have no part in any row, whatever they hold.  A NaN
- * or an infinity in a key, value or gradient that some query sees spreads to all
+ * Keys that no query sees, and queries that see no key, have no part in any other
+ * row, whatever they and their gradients hold.  A NaN or an infinity in a key or
+ * value that some query sees, or in such a query's gradient, spreads to all
  * rows that see it and, times a probability of 0, may reach rows of the same
  * sequence that do not.
  *

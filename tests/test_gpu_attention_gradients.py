@@ -56,3 +56,28 @@ def test_against_differences_along_the_gradient(kind):
         tol = float(getattr(e, "bound_" + name).norm())       # of the whole error's norm; the difference is off by 1e-5 of itself
         assert tol < 0.1 * diff
         assert abs(float((f64(got[i]) * d).sum()) - diff) <= tol + 1e-5 * diff, name
+
+
+@pytest.mark.parametrize("heads", [(2, 1), (4, 4)])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("ql,kl,window,sinks", [([90], [40], 0, 0), ([300, 20], [200, 20], 0, 0), ([70, 5], [30, 0], 16, 2)])
+def test_rows_that_see_nothing_whatever_they_hold(ql, kl, window, sinks, hd, heads):
+    """Queries and gradients of rows that see no key hold NaN or infinities: zero gradients, and no other one changes."""
+    starts = lambda n: torch.tensor([sum(n[:i]) for i in range(len(n) + 1)], dtype=torch.int32, device="cuda")  # noqa: E731
+    g = torch.Generator().manual_seed(11)
+    new = lambda n, h: torch.randn(n, h, hd, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    q, k, v, do = new(sum(ql), heads[0]), new(sum(kl), heads[1]), new(sum(kl), heads[1]), new(sum(ql), heads[0])
+    gone = torch.zeros(sum(ql), dtype=torch.bool, device="cuda")
+    for i, (n, m) in enumerate(zip(ql, kl)):
+        gone[sum(ql[:i]):sum(ql[:i]) + max(0, n - m)] = True
+    seqs, mask = (starts(ql), starts(kl)), dict(window=window, sinks=sinks)
+
+    def path(fill):
+        q[gone], do[gone] = fill, -fill
+        o, lse = puro.attention(q, k, v, *seqs, **mask)
+        return (o, lse) + puro.attention_backward(do, q, k, v, o, lse, *seqs, **mask)
+
+    want = path(0.0)
+    assert not bool(want[0][gone].any()) and not bool(want[2][gone].any()) and all(bool(t.isfinite().all()) for t in want[2:])
+    for fill in (float("nan"), float("inf")):
+        assert all(torch.equal(a, b) for a, b in zip(path(fill), want))
