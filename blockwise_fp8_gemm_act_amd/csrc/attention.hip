@@ -56,10 +56,6 @@ __device__ __forceinline__ float tile_max(const f32x16 &s) {
 }
 
 // ---------------------------------------------------------------- many queries
-constexpr int kFwdWaves = 8, kFwdKeys = 64;
-// (query, head) rows of a workgroup; `pack` heads of a group by kFwdRows / pack queries.
-constexpr int kFwdRows = 32 * kFwdWaves;
-
 // Bound by the matrix cores: 4 head_dim operations a visible pair, against 2 bytes of
 // keys and values that a block reads for every 256 of its rows.  Beside them an
 // exponential and four other vector operations a pair want as long as the products at
@@ -279,8 +275,6 @@ __global__ void __launch_bounds__(64 * kFwdWaves, kHd == 64 ? 4 : 2) attn_kernel
 }
 
 // ---------------------------------------------------------------- few queries
-constexpr int kSplitWaves = 4, kSplitRows = 32, kSplitKeys = 32;
-
 // Partials of one (tile, key head, split): kSplitRows rows of kHd values, then m
 // and l of each row.
 template <int kHd>
@@ -466,7 +460,6 @@ __global__ void __launch_bounds__(64 * kSplitWaves) attn_split_kernel(AttnArgs a
 
 // One wave a row: lanes first as splits (the maxima and sums of up to 128 of them),
 // then as columns, kHd / 64 each, eight splits' partials in flight.
-constexpr int kMostSplits = 128;
 template <int kHd>
 __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int splits) {
   constexpr int kPer = kHd / 64;
@@ -525,17 +518,16 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int splits) 
 
 template <int kHd>
 hipError_t launch(const AttnArgs &a, const AttnPlan &plan, hipStream_t stream) {
+  const auto grid = [](int64_t blocks) { return dim3((unsigned)blocks); };
   if (!plan.split) {
-    const int64_t blocks = (int64_t)Order(plan.slots, a.sequences, a.window).count() * (a.q_heads / plan.pack);
-    attn_kernel<kHd><<<dim3((unsigned)blocks), dim3(64 * kFwdWaves), 0, stream>>>(a, plan.slots, plan.pack);
+    attn_kernel<kHd><<<grid(fwd_blocks(plan, a.q_heads, a.sequences, a.window)), dim3(64 * kFwdWaves), 0, stream>>>(
+        a, plan.slots, plan.pack);
     return hipGetLastError();
   }
-  attn_split_kernel<kHd><<<dim3((unsigned)((int64_t)plan.slots * a.k_heads * plan.splits)), dim3(64 * kSplitWaves), 0,
-                           stream>>>(a, plan.splits);
+  attn_split_kernel<kHd><<<grid(split_blocks(plan, a.k_heads)), dim3(64 * kSplitWaves), 0, stream>>>(a, plan.splits);
   if (hipError_t e = hipGetLastError()) return e;
   if (plan.splits > 1) {
-    attn_join_kernel<kHd><<<dim3((unsigned)((int64_t)plan.slots * a.k_heads * (kSplitRows / 4))), dim3(256), 0, stream>>>(
-        a, plan.splits);
+    attn_join_kernel<kHd><<<grid(split_join_blocks(plan, a.k_heads)), dim3(256), 0, stream>>>(a, plan.splits);
     return hipGetLastError();
   }
   return hipSuccess;
@@ -543,64 +535,7 @@ hipError_t launch(const AttnArgs &a, const AttnPlan &plan, hipStream_t stream) {
 
 }  // namespace
 
-// Both kernels' times are estimated from the average sequence and the smaller wins.  A
-// workgroup costs a fixed time and one for each 64 (128) keys it walks, and 256 of them
-// run at a time; the constants, in us, are fitted to 47 shapes of heads of 128 and 97 of
-// heads of 64, with 1 to 64 sequences, 8 to 4096 queries and up to 16384 earlier keys (97
-// shapes: on average 0.3% slower than the better kernel, 17% at worst).  Examples (many /
-// few queries' kernel), 16 and 8 heads of 128: 64 x 8 queries over 2056 keys 266 / 127 us;
-// 16 x 64 over 2112 67 / 63; 8 x 512 over 512 34 / 66; 1 x 4096 over 4096 113 / 229;
-// 1 x 512 over 16896 755 / 209.
-AttnPlan plan_attention(const puro_attention_shape &a) {
-  AttnPlan p{};
-  const double units = 256.0;
-  const int64_t group = a.q_heads / a.k_heads;
-  const int64_t few = a.q_tokens * group / kSplitRows + a.sequences;
-  const double ql = (double)a.q_tokens / a.sequences;
-  double kl = a.max_k > 0 ? (double)a.max_k : (double)a.k_tokens / a.sequences;
-  const double far = a.window > 0 ? (double)(a.window + a.sinks) : kl;
-  // Keys that a tile of `rows` queries walks, at most and on average.
-  auto most = [&](double rows) {
-    const double see = far + (rows < ql ? rows : ql);
-    return kl < see ? kl : see;
-  };
-  auto mean = [&](double rows) {
-    const double all = kl > ql / 2 ? kl - ql / 2 : 0;
-    return all < most(rows) ? all : most(rows);
-  };
-
-  // Few queries' kernel: splits fill the units once, empty tiles counted (a 257th
-  // workgroup waits for a place: 16 x 16 queries over 2064 keys took 38 us split in two,
-  // 30 us whole), and hold at least 4 chunks of keys a wave.
-  const double wf = (double)a.sequences * (int64_t)((ql * group + kSplitRows - 1) / kSplitRows) * a.k_heads;
-  int64_t splits = 256 / (few * a.k_heads);
-  const int64_t longest = (int64_t)(most(1) / (4 * kSplitWaves * kSplitKeys));
-  if (splits > longest) splits = longest;
-  if (splits > kMostSplits) splits = kMostSplits;
-  if (splits < 1) splits = 1;
-  const bool wide = a.head_dim == 128;
-  const double per_few = wide ? 1.5 : 0.9, per_many = wide ? 1.6 : 1.3, start_few = wide ? 4 : 3, start_many = wide ? 5 : 6;
-  const double walk_few = wf < units ? most(1) / splits : mean(1);
-  const double t_few = (wf < units ? 1 : wf / units) * (start_few + per_few * walk_few / (kSplitWaves * kSplitKeys));
-  // Heads that share keys share a workgroup: lower blocks see fewer keys that only some
-  // of their queries see (heads alone / in twos / in fours, us: 287 / 280 / - at 4 x 4096
-  // tokens, 194 / 186 / - at 16381 with a window of 1024, 16 and 8 heads of 128; - / 51 /
-  // 46 at 8192 with a window of 512, 16 and 4 heads of 64).
-  p.pack = group % 4 == 0 ? 4 : group % 2 == 0 ? 2 : 1;
-  const int tall = kFwdRows / p.pack;
-  const double wm = (double)a.sequences * (int64_t)((ql + tall - 1) / tall) * (a.q_heads / p.pack);
-  const double walk_many = wm < units ? most(tall) : mean(tall);
-  const double t_many = (wm < units ? 1 : wm / units) * (start_many + per_many * walk_many / kFwdKeys);
-
-  p.split = t_few < t_many;
-  p.splits = 1;
-  p.slots = (int)(p.split ? few : a.q_tokens / tall + a.sequences);
-  if (p.split && splits > 1) {
-    p.splits = (int)splits;
-    p.ws_bytes = (size_t)few * (size_t)a.k_heads * (size_t)splits * (size_t)kSplitRows * (size_t)(a.head_dim + 2) * 4;
-  }
-  return p;
-}
+AttnPlan plan_attention(const puro_attention_shape &a) { return forward_plan(a); }
 
 hipError_t run_attention(const AttnArgs &a, int head_dim, const AttnPlan &plan, hipStream_t stream) {
   return head_dim == 128 ? launch<128>(a, plan, stream) : launch<64>(a, plan, stream);

@@ -24,8 +24,6 @@ __device__ __forceinline__ f32x16 splat(float x) {
 }
 
 // ---------------------------------------------------------------- dq
-constexpr int kDqWaves = 4, kDqRows = 32 * kDqWaves, kDqKeys = 64;
-
 // Three products a pair (S, do v, dS k): bound by the matrix cores, busy 61% of the time
 // (counters, 4 x 4096 tokens, 16 and 8 heads of 128: 412 GFLOP in 352 us).  Two workgroups
 // a unit at heads of 128, whose waves fill each other's gaps; of heads of 64 four.
@@ -246,8 +244,6 @@ __global__ void __launch_bounds__(64 * kDqWaves, kHd == 64 ? 4 : 2) attn_dq_kern
 }
 
 // ---------------------------------------------------------------- dk, dv
-constexpr int kDkWaves = 4, kDkRows = 32 * kDkWaves, kDkQueries = 64;
-
 // Four products a pair (S, do v, P^T do, dS^T q).  Keys stand as columns here, so that a
 // lane owns a key, and P and dS are again operands in place.  A wave holds 32 keys and
 // values (64 registers at heads of 128) and the sums of their gradients (128), which leaves
@@ -257,23 +253,7 @@ constexpr int kDkWaves = 4, kDkRows = 32 * kDkWaves, kDkQueries = 64;
 // first 973; copies between the products 903; starting values in the accumulators 823 to 863
 // from card to card.  One wave a SIMD with twice the registers: 1150 where this took 979.
 //
-// Work on one block of 128 keys and one key head: tiles of 64 queries of each head of
-// the group.  `near` tiles hold the queries that have the block in their window; for a
-// block of first keys `far` tiles hold the later queries, which see the first keys
-// only.  Without far work such a block would walk its whole sequence while all others
-// walk a window.  Either walk is cut into parts where it is long for the card (many
-// heads over few keys; a long sequence past its first keys), which leave fp32 partials
-// for the join.
-struct DkPlan {
-  int slots;          // key blocks, empty ones included
-  int parts;          // of each near walk
-  int far_blocks;     // key blocks of a sequence that hold first keys; 0: no far work
-  int far_slots;      // parts of far walks over all sequences, empty ones included
-  size_t near_at, edge_at, far_at, floats;   // partials in the workspace, in floats: of near walks, of near walks over
-                                             // first keys that are not cut, of far walks
-};
-constexpr int kFarChunk = 24;     // tiles of a far part: about a near walk's, whose workgroups run beside it
-
+// DkPlan says what a workgroup's work is.
 struct Walk {
   int q_lo, q_hi;     // queries of the sequence
   int tile0, tiles;
@@ -605,71 +585,21 @@ __global__ void __launch_bounds__(256) attn_dkdv_join_kernel(AttnArgs a, DkPlan 
   *reinterpret_cast<u32x4 *>(a.dv + row * a.dvs + (int64_t)hk * kHd + c) = v;
 }
 
-// The plan from sizes alone (host).
-DkPlan plan_dk(int64_t q_tokens, int64_t k_tokens, int64_t sequences, int64_t q_heads, int64_t k_heads, int64_t head_dim,
-               int64_t window, int64_t sinks) {
-  DkPlan p{};
-  const int64_t floats = 2 * kDkRows * head_dim;
-  p.slots = (int)(k_tokens / kDkRows + sequences);
-  const int64_t group = q_heads / k_heads;
-  const int64_t per_seq = (q_tokens + sequences - 1) / sequences;
-  // Near walks are cut into the number of parts with the least estimated time, in us: the
-  // longest part alone, or all parts over the places of the card (256 compute units, two
-  // workgroups each, three with heads of 64), and the partials' way through memory.  The
-  // constants are fitted to 112 shapes of 1 to 64 sequences of 128 to 16384 tokens: 0.8%
-  // slower on average than the best number, 9% at worst.  The whole backward call, causal,
-  // 1 / 2 / 3 / 4 / 6 / 8 parts, us: 4096 tokens, 16 and 8 heads of 128: 380 / 302 / 276 /
-  // 282 / 309 / 351; 4 x 4096: 860 / 932 / 979 / 1033 / 1138 / 1263; 8 x 2048, 8 heads and 1
-  // of 128: 625 / 384 / 319 / 291 / 267 / 281; 8192, 16 and 4 of 64: 839 / 596 / 528 / 502 /
-  // 506 / 505.
-  const bool windowed = window > 0 && window + kDkRows < per_seq;
-  const int64_t seen = windowed ? window + kDkRows : per_seq;
-  const int64_t longest = (seen + kDkQueries - 1) / kDkQueries * group;
-  const double average = windowed ? (double)longest : (double)(longest + group) / 2;
-  const int64_t keys = (k_tokens + sequences - 1) / sequences;
-  const double blocks = (double)sequences * ((keys + kDkRows - 1) / kDkRows) * k_heads;
-  double best = 0;
-  for (int parts : {1, 2, 3, 4, 6, 8, 12, 16}) {
-    if (parts > 1 && longest < 2 * parts) break;
-    const double alone = 2.0 * longest / parts + 2;
-    const double all = 3.0 * blocks * (average + 2 * parts) / (head_dim == 128 ? 512 : 768);
-    const double time = (alone > all ? alone : all) + (parts > 1 ? 4 + 0.08 * blocks * parts * head_dim / 128 : 0);
-    if (parts > 1 && time >= best) continue;
-    best = time;
-    p.parts = parts;
-  }
-  p.near_at = ((size_t)2 * q_heads * q_tokens + 63) / 64 * 64;
-  p.floats = p.near_at + (p.parts > 1 ? (size_t)p.slots * k_heads * p.parts * floats : 0);
-  p.edge_at = p.far_at = p.floats;
-  // Far work pays where a sequence may be several windows long; many first keys make
-  // enough blocks by themselves, and partials for them would be large.
-  if (window > 0 && sinks > 0 && sinks <= 2 * kDkRows && q_tokens >= 2 * (window + kDkRows)) {
-    p.far_blocks = (int)((sinks + kDkRows - 1) / kDkRows);
-    p.far_slots = (int)(q_tokens * group / (kFarChunk * kDkQueries) + sequences);
-    p.far_at = p.edge_at + (p.parts == 1 ? (size_t)sequences * p.far_blocks * k_heads * floats : 0);
-    p.floats = p.far_at + (size_t)p.far_slots * p.far_blocks * k_heads * floats;
-  }
-  return p;
-}
-
 template <int kHd>
 hipError_t launch(const AttnArgs &a, hipStream_t stream) {
+  const auto grid = [](int64_t blocks) { return dim3((unsigned)blocks); };
   if (a.q_tokens > 0) {
-    const int pack = a.group % 4 == 0 ? 4 : a.group % 2 == 0 ? 2 : 1, slots = a.q_tokens / (kDqRows / pack) + a.sequences;
-    attn_dq_kernel<kHd><<<dim3((unsigned)((int64_t)Order(slots, a.sequences, a.window).count() * (a.q_heads / pack))),
-                          dim3(64 * kDqWaves), 0, stream>>>(a, slots, pack);
+    const int pack = pack_of(a.group), slots = dq_slots(a.q_tokens, a.sequences, pack);
+    attn_dq_kernel<kHd><<<grid(dq_blocks(slots, pack, a.q_heads, a.sequences, a.window)), dim3(64 * kDqWaves), 0, stream>>>(
+        a, slots, pack);
     if (hipError_t e = hipGetLastError()) return e;
   }
   if (a.k_tokens == 0) return hipSuccess;
   const DkPlan plan = plan_dk(a.q_tokens, a.k_tokens, a.sequences, a.q_heads, a.k_heads, kHd, a.window, a.sinks);
-  const int64_t near = (int64_t)Order(plan.slots, a.sequences, a.window).count() * plan.parts;
-  const int64_t items = (int64_t)plan.far_slots * plan.far_blocks + near;
-  attn_dkdv_kernel<kHd><<<dim3((unsigned)(items * a.k_heads)), dim3(64 * kDkWaves), 0, stream>>>(a, plan);
+  attn_dkdv_kernel<kHd><<<grid(dk_blocks(plan, a.k_heads, a.sequences, a.window)), dim3(64 * kDkWaves), 0, stream>>>(a, plan);
   if (hipError_t e = hipGetLastError()) return e;
   if (plan.parts > 1 || plan.far_blocks > 0) {
-    const int chunks = kDkRows / (256 / (kHd / 8));
-    const int64_t blocks = (int64_t)plan.slots * chunks * a.k_heads;
-    attn_dkdv_join_kernel<kHd><<<dim3((unsigned)blocks), dim3(256), 0, stream>>>(a, plan);
+    attn_dkdv_join_kernel<kHd><<<grid(dk_join_blocks(plan, a.k_heads, kHd)), dim3(256), 0, stream>>>(a, plan);
     return hipGetLastError();
   }
   return hipSuccess;

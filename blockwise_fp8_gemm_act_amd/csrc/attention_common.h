@@ -11,6 +11,7 @@
 // follows.
 #pragma once
 
+#include "attention_plan.h"
 #include "device_common.h"
 #include "launch_attention.h"
 
@@ -98,21 +99,6 @@ __device__ __forceinline__ Seq find_seq(const AttnArgs &a, const int32_t *start,
   const int most = k1 > k0 ? k1 - k0 : 0;
   return Seq{q0, q1 > q0 ? q1 - q0 : 0, k0, clampi(kl, 0, most)};
 }
-
-// Order in which tiles start.  Without a window a tile's work grows along its sequence:
-// the x-th numbers of `sequences` equal parts of the number line come before the next of
-// any, so that (with sequences alike) those that walk far start first in all of them and
-// the short ones fill the end.  A permutation in any case, up to numbers past the end,
-// which are no tiles.  4 x 4096 tokens backward: 1094 -> 975 us.  With a window the work
-// is even, and neighbours in the sequence share keys: as numbered.
-struct Order {
-  int slots, parts;
-  __device__ __host__ __forceinline__ Order(int slots, int sequences, int window)
-      : slots(slots), parts(window > 0 ? 1 : sequences) {}
-  __device__ __host__ __forceinline__ int each() const { return (slots + parts - 1) / parts; }
-  __device__ __host__ __forceinline__ int count() const { return each() * parts; }
-  __device__ __forceinline__ int operator()(int x) const { return x % parts * each() + x / parts; }
-};
 
 // ---------------------------------------------------------------- mask
 // The key tiles that a block of queries at positions p_lo .. p_hi looks at, `unit`
