@@ -140,9 +140,11 @@ bool attention_shape_ok(const puro_attention_shape *a, bool backward) {
   if (a->sequences < 1 || a->sequences > (1 << 24) || a->q_heads < 1 || a->k_heads < 1 || a->q_heads > 65536 ||
       a->q_heads % a->k_heads != 0)
     return false;
-  // Every launch stays below 2^32 threads: at most 2 (tokens + 512 sequences) heads.
-  if ((a->q_tokens + 512 * a->sequences) * a->q_heads > kMaxDim) return false;
-  if (backward && (a->k_tokens + 512 * a->sequences) * a->k_heads > kMaxDim) return false;
+  // What the runtime takes, fewer than 2^32 threads: forward at most 2 (tokens + 512 sequences) heads, backward a third
+  // of the query heads' more for the far queries of first keys; the join of its partials takes any number in strides.
+  const int64_t most = backward ? kMaxDim / 4 * 3 : kMaxDim;
+  if ((a->q_tokens + 512 * a->sequences) * a->q_heads > most) return false;
+  if (backward && (a->k_tokens + 512 * a->sequences) * a->k_heads > most) return false;
   if (a->max_k < 0 || a->window < 0 || a->sinks < 0) return false;
   const int64_t qw = a->q_heads * a->head_dim, kw = a->k_heads * a->head_dim;
   if (!strided_ok(a->q_tokens, qw, a->q_stride) || !strided_ok(a->k_tokens, kw, a->k_stride) ||

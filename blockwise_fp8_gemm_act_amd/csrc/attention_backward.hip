@@ -539,50 +539,53 @@ __global__ void __launch_bounds__(64 * kDkWaves, 2) attn_dkdv_kernel(AttnArgs a,
   }
 }
 
-// Sums the partials of a key block in order: 8 columns a thread.
+// Sums the partials of a key block in order: 8 columns a thread, shares of a block in strides.
 template <int kHd>
-__global__ void __launch_bounds__(256) attn_dkdv_join_kernel(AttnArgs a, DkPlan plan) {
+__global__ void __launch_bounds__(256) attn_dkdv_join_kernel(AttnArgs a, DkPlan plan, int shares) {
   constexpr int kThreads = kHd / 8, kRows = 256 / kThreads, kChunks = kDkRows / kRows;
-  const int hk = (int)(blockIdx.x % a.k_heads);
-  const int rest = (int)(blockIdx.x / a.k_heads);
-  const int number = rest / kChunks;
-  int slot = number;
-  int s;
-  const Seq sq = find_seq(a, a.k_start, 1, kDkRows, slot, s);
-  const int fars = slot < plan.far_blocks && (int64_t)slot * kDkRows < sq.kl ? far_parts(a, plan, sq, s, slot) : 0;
-  if (plan.parts == 1 && fars == 0) return;
-  const int r = (rest % kChunks) * kRows + (int)threadIdx.x / kThreads, c = 8 * ((int)threadIdx.x % kThreads);
-  if ((int64_t)slot * kDkRows + r >= sq.kl) return;
-  float x[2][8] = {};
-  auto add = [&](const float *from) {
+  for (int share = blockIdx.x; share < shares; share += gridDim.x) {
+    const int hk = (int)(share % a.k_heads);
+    const int rest = (int)(share / a.k_heads);
+    const int number = rest / kChunks;
+    int slot = number;
+    int s;
+    const Seq sq = find_seq(a, a.k_start, 1, kDkRows, slot, s);
+    const int fars = slot < plan.far_blocks && (int64_t)slot * kDkRows < sq.kl ? far_parts(a, plan, sq, s, slot) : 0;
+    if ((int64_t)slot * kDkRows >= sq.kl || (plan.parts == 1 && fars == 0)) continue;
+    const int r = (rest % kChunks) * kRows + (int)threadIdx.x / kThreads, c = 8 * ((int)threadIdx.x % kThreads);
+    float x[2][8] = {};
+    auto add = [&](const float *from) {
 #pragma unroll
-    for (int w = 0; w < 2; ++w)
+      for (int w = 0; w < 2; ++w)
 #pragma unroll
-      for (int j = 0; j < 8; j += 4) {
-        const f32x4 v = *reinterpret_cast<const f32x4 *>(from + (w * kDkRows + r) * kHd + c + j);
+        for (int j = 0; j < 8; j += 4) {
+          const f32x4 v = *reinterpret_cast<const f32x4 *>(from + (w * kDkRows + r) * kHd + c + j);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[w][j + e] += v[e];
+          for (int e = 0; e < 4; ++e) x[w][j + e] += v[e];
+        }
+    };
+    if (plan.parts > 1)
+      for (int p = 0; p < plan.parts; ++p)
+        add(a.ws + plan.near_at + ((size_t)(number * a.k_heads + hk) * plan.parts + p) * part_floats<kHd>());
+    else
+      add(a.ws + plan.edge_at + (size_t)((s * plan.far_blocks + slot) * a.k_heads + hk) * part_floats<kHd>());
+    if (fars > 0) {
+      const int f0 = far_first(a, sq.q0, s);
+      for (int p = 0; p < fars; ++p)
+        add(a.ws + plan.far_at + (size_t)(((f0 + p) * plan.far_blocks + slot) * a.k_heads + hk) * part_floats<kHd>());
+    }
+    if (slot * kDkRows + r < sq.kl) {       // a partial has all rows of its block
+      const int64_t row = sq.k0 + slot * kDkRows + r;
+      u32x4 k, v;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        k[j] = pack_bf16(x[0][2 * j] * a.scale, x[0][2 * j + 1] * a.scale);
+        v[j] = pack_bf16(x[1][2 * j], x[1][2 * j + 1]);
       }
-  };
-  if (plan.parts > 1)
-    for (int p = 0; p < plan.parts; ++p)
-      add(a.ws + plan.near_at + ((size_t)(number * a.k_heads + hk) * plan.parts + p) * part_floats<kHd>());
-  else
-    add(a.ws + plan.edge_at + (size_t)((s * plan.far_blocks + slot) * a.k_heads + hk) * part_floats<kHd>());
-  if (fars > 0) {
-    const int f0 = far_first(a, sq.q0, s);
-    for (int p = 0; p < fars; ++p)
-      add(a.ws + plan.far_at + (size_t)(((f0 + p) * plan.far_blocks + slot) * a.k_heads + hk) * part_floats<kHd>());
+      *reinterpret_cast<u32x4 *>(a.dk + row * a.dks + (int64_t)hk * kHd + c) = k;
+      *reinterpret_cast<u32x4 *>(a.dv + row * a.dvs + (int64_t)hk * kHd + c) = v;
+    }
   }
-  const int64_t row = sq.k0 + slot * kDkRows + r;
-  u32x4 k, v;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    k[j] = pack_bf16(x[0][2 * j] * a.scale, x[0][2 * j + 1] * a.scale);
-    v[j] = pack_bf16(x[1][2 * j], x[1][2 * j + 1]);
-  }
-  *reinterpret_cast<u32x4 *>(a.dk + row * a.dks + (int64_t)hk * kHd + c) = k;
-  *reinterpret_cast<u32x4 *>(a.dv + row * a.dvs + (int64_t)hk * kHd + c) = v;
 }
 
 template <int kHd>
@@ -599,7 +602,8 @@ hipError_t launch(const AttnArgs &a, hipStream_t stream) {
   attn_dkdv_kernel<kHd><<<grid(dk_blocks(plan, a.k_heads, a.sequences, a.window)), dim3(64 * kDkWaves), 0, stream>>>(a, plan);
   if (hipError_t e = hipGetLastError()) return e;
   if (plan.parts > 1 || plan.far_blocks > 0) {
-    attn_dkdv_join_kernel<kHd><<<grid(dk_join_blocks(plan, a.k_heads, kHd)), dim3(256), 0, stream>>>(a, plan);
+    attn_dkdv_join_kernel<kHd><<<grid(dk_join_blocks(plan, a.k_heads, kHd)), dim3(256), 0, stream>>>(
+        a, plan, (int)dk_join_shares(plan, a.k_heads, kHd));
     return hipGetLastError();
   }
   return hipSuccess;

@@ -178,8 +178,34 @@ inline DkPlan plan_dk(int64_t q_tokens, int64_t k_tokens, int64_t sequences, int
 inline int64_t dk_blocks(const DkPlan &p, int64_t k_heads, int sequences, int window) {
   return ((int64_t)p.far_slots * p.far_blocks + (int64_t)Order(p.slots, sequences, window).count() * p.parts) * k_heads;
 }
-inline int64_t dk_join_blocks(const DkPlan &p, int64_t k_heads, int64_t head_dim) {      // 8 columns a thread
+// The join's share of a workgroup: 256 threads of 8 columns.  Its workgroups stride over the shares, since the runtime takes
+// fewer than 2^32 threads.
+inline int64_t dk_join_shares(const DkPlan &p, int64_t k_heads, int64_t head_dim) {
   return (int64_t)p.slots * (kDkRows / (256 / (head_dim / 8))) * k_heads;
 }
+inline int64_t dk_join_blocks(const DkPlan &p, int64_t k_heads, int64_t head_dim) {
+  const int64_t shares = dk_join_shares(p, k_heads, head_dim), most = (int64_t(1) << 24) - 1;
+  return shares < most ? shares : most;
+}
+
+// ---------------------------------------------------------------- rotation
+constexpr int kRopeWaves = 4;      // waves of a workgroup
+
+struct RopePlan {
+  int parts;          // waves a token
+  int64_t tokens;     // of a launch, at most: the runtime takes fewer than 2^32 threads
+};
+
+inline RopePlan plan_rope(int64_t tokens, int64_t heads, int64_t head_dim) {
+  const int64_t teams = 512 / head_dim, groups = (heads + teams - 1) / teams;       // heads that a wave reads at once
+  // Waves a token: one where the tokens alone fill the card, one per group of heads where
+  // they are few, so that no wave loops.  Norms of 24 heads of 128, back to back in a graph,
+  // 1 / 2 / 3 / 6 waves, us: 32 tokens 4.7 / 3.5 / 3.2 / 3.0; 512 tokens 5.2 / 4.0 / 4.1 /
+  // 4.2; 2048 tokens 8.4 / 8.1 / 7.9 / 9.5; 4096 tokens 11.4 / 12.6 / 12.9 / 15.6; 16384
+  // tokens 37.1 / 38.6 / 42.7 / 60.5.
+  const int64_t parts = tokens >= 4096 ? 1 : tokens >= 512 ? 2 : groups;
+  return RopePlan{(int)(parts < groups ? parts : groups), int64_t(1) << 25};
+}
+inline int64_t rope_blocks(const RopePlan &p, int64_t tokens) { return (tokens * p.parts + kRopeWaves - 1) / kRopeWaves; }
 
 }  // namespace puro

@@ -14,6 +14,7 @@
 // pairs of the half layout lie rot/2 elements apart: the partner's raw 16 bytes come from
 // the lane rot/16 away by a lane permute, not by a second read.  A token's cosines and
 // sines are loaded once per wave and used for all its heads.
+#include "attention_plan.h"
 #include "device_common.h"
 #include "launch_attention.h"
 
@@ -23,7 +24,7 @@ namespace {
 typedef float v2f __attribute__((ext_vector_type(2)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 
-constexpr int kWaves = 4;      // waves per workgroup
+constexpr int kWaves = kRopeWaves;
 
 __device__ __forceinline__ uint32_t pack2_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f){a, b}, v2bf));
@@ -125,15 +126,15 @@ struct Turn {
 };
 
 // ---------------------------------------------------------------- forward
-// `parts` waves share a token: each takes every parts-th group of heads.  kBatch
-// heads a lane are in flight at once.
+// Tokens from `first` on.  `parts` waves share a token: each takes every parts-th group
+// of heads.  kBatch heads a lane are in flight at once.
 template <int kHd, bool kInter, bool kNorm, bool kAppend>
-__global__ void __launch_bounds__(64 * kWaves) rope_kernel(RopeArgs a, int parts) {
+__global__ void __launch_bounds__(64 * kWaves) rope_kernel(RopeArgs a, int parts, int64_t first) {
   constexpr int kTeam = kHd / 8, kTeams = 64 / kTeam, kBatch = 3;
   const int lane = threadIdx.x & 63;
   const int64_t w = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t = w / parts;
-  const int part = (int)(w - t * parts);
+  const int64_t in = w / parts, t = first + in;
+  const int part = (int)(w - in * parts);
   if (t >= a.tokens) return;
   const int c = lane % kTeam, team = lane / kTeam;
   const int normed = a.heads_q + a.heads_k, heads = normed + a.heads_v;
@@ -200,26 +201,20 @@ __global__ void __launch_bounds__(64 * kWaves) rope_kernel(RopeArgs a, int parts
 
 template <int kHd, bool kInter>
 hipError_t launch_rope(const RopeArgs &a, hipStream_t stream) {
-  constexpr int kTeams = 64 / (kHd / 8);
-  const int heads = a.heads_q + a.heads_k + a.heads_v;
-  const int groups = (heads + kTeams - 1) / kTeams;
-  // Waves a token: one where the tokens alone fill the card, one per group of heads where
-  // they are few, so that no wave loops.  Norms of 24 heads of 128, back to back in a graph,
-  // 1 / 2 / 3 / 6 waves, us: 32 tokens 4.7 / 3.5 / 3.2 / 3.0; 512 tokens 5.2 / 4.0 / 4.1 /
-  // 4.2; 2048 tokens 8.4 / 8.1 / 7.9 / 9.5; 4096 tokens 11.4 / 12.6 / 12.9 / 15.6; 16384
-  // tokens 37.1 / 38.6 / 42.7 / 60.5.
-  int parts = a.tokens >= 4096 ? 1 : a.tokens >= 512 ? 2 : groups;
-  if (parts > groups) parts = groups;
-  const int64_t blocks = (a.tokens * parts + kWaves - 1) / kWaves;
-  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)blocks), block(64 * kWaves);
-  if (a.rows)
-    rope_kernel<kHd, kInter, true, true><<<grid, block, 0, stream>>>(a, parts);
-  else if (a.wq)
-    rope_kernel<kHd, kInter, true, false><<<grid, block, 0, stream>>>(a, parts);
-  else
-    rope_kernel<kHd, kInter, false, false><<<grid, block, 0, stream>>>(a, parts);
-  return hipGetLastError();
+  const RopePlan plan = plan_rope(a.tokens, a.heads_q + a.heads_k + a.heads_v, kHd);
+  const dim3 block(64 * kWaves);
+  for (int64_t first = 0; first < a.tokens; first += plan.tokens) {
+    const int64_t left = a.tokens - first, n = left < plan.tokens ? left : plan.tokens;
+    const dim3 grid((unsigned)rope_blocks(plan, n));
+    if (a.rows)
+      rope_kernel<kHd, kInter, true, true><<<grid, block, 0, stream>>>(a, plan.parts, first);
+    else if (a.wq)
+      rope_kernel<kHd, kInter, true, false><<<grid, block, 0, stream>>>(a, plan.parts, first);
+    else
+      rope_kernel<kHd, kInter, false, false><<<grid, block, 0, stream>>>(a, plan.parts, first);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  return hipSuccess;
 }
 
 // ---------------------------------------------------------------- backward

@@ -160,6 +160,10 @@ puro_status puro_qk_norm_rope_backward(const puro_rotation *r, const uint16_t *d
  *
  * Heads.  k_heads divides q_heads; query head h reads key head h / (q_heads /
  * k_heads).
+ *
+ * Sizes.  At most 2^30 query and key rows, 2^24 sequences and 2^16 query heads;
+ * (q_tokens + 512 sequences) q_heads below 2^31, in the backward call three
+ * quarters of it, and (k_tokens + 512 sequences) k_heads likewise.
  */
 typedef struct {
     int64_t q_tokens, k_tokens, sequences;

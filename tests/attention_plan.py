@@ -42,6 +42,11 @@ class Plans:
     def backward(self, shape):
         return Backward(*self._ask(self.lib.backward, shape))
 
+    def rope(self, tokens, heads, head_dim):
+        out = (ctypes.c_int64 * 3)()
+        self.lib.rope(ctypes.c_int64(tokens), ctypes.c_int64(heads), ctypes.c_int64(head_dim), out)
+        return list(out)
+
 
 def shape(qh, kh, hd, q_tokens, k_tokens, sequences=1, window=0, sinks=0, max_k=0):
     import blockwise_fp8_gemm_act_amd as puro

@@ -46,3 +46,11 @@ extern "C" void backward(const puro_attention_shape *s, int64_t *out) {
   out[4] = dk_blocks(p, a.k_heads, a.sequences, a.window);
   out[5] = p.parts > 1 || p.far_blocks > 0 ? dk_join_blocks(p, a.k_heads, s->head_dim) : 0;
 }
+
+// out: waves a token, launches, workgroups of 256 threads of the largest.
+extern "C" void rope(int64_t tokens, int64_t heads, int64_t head_dim, int64_t *out) {
+  const RopePlan p = plan_rope(tokens, heads, head_dim);
+  out[0] = p.parts;
+  out[1] = (tokens + p.tokens - 1) / p.tokens;
+  out[2] = rope_blocks(p, tokens < p.tokens ? tokens : p.tokens);
+}

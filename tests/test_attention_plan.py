@@ -32,3 +32,47 @@ def test_shapes_of_the_kernel_for_few_queries(plans, case):
     qh, kh, hd, queries, n, kl = case
     p = plans.forward(ap.shape(qh, kh, hd, queries * n, kl * n, n))
     assert p.few == 1 and p.splits == (7 if n == 1 else 1)
+
+
+THREADS = 1 << 32          # a launch of this many is refused by the runtime
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("heads", [(1, 1), (2, 1), (16, 8), (65536, 1), (65536, 65536)])
+@pytest.mark.parametrize("sequences", [1, 2, 1000, 1 << 16, 1 << 22])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 256), (1000, 4)])
+@pytest.mark.parametrize("backward", [False, True])
+def test_largest_launches(plans, backward, hd, heads, sequences, window, sinks):
+    """Grids at the largest token counts that a call accepts."""
+    import blockwise_fp8_gemm_act_amd as puro
+    import torch
+    qh, kh = heads
+    limit = (1 << 31) // 4 * 3 if backward else 1 << 31
+    q_most, k_most = (min(1 << 30, (1 << 40) // (h * hd), (limit - 4) // h - 512 * sequences) for h in heads)
+    if q_most < 1 or k_most < 1:
+        return
+    at = [1 << 56 | i << 52 for i in range(12)]
+    for qt, kt in ((q_most, k_most), (q_most, 300), (600, k_most), (600, 300)):
+        s = ap.shape(qh, kh, hd, min(qt, q_most), min(kt, k_most), sequences, window, sinks)
+        if backward:
+            p = plans.backward(s)
+            threads = [256 * n for n in (p.dq_blocks, p.dk_blocks, p.join_blocks)]
+            accepted = lambda s: puro.puro_attention_backward(s, *at, 1 << 62, None)  # noqa: E731
+        else:
+            p = plans.forward(s)
+            threads = [p.threads * p.blocks, 256 * p.join_blocks]
+            accepted = lambda s: puro.puro_attention(s, *at[:9], 1 << 62, None)  # noqa: E731
+        assert max(threads) < THREADS, vars(p)
+        if not torch.cuda.is_available() and qh * hd < 1 << 23:          # stopped only by the missing device; one more is refused
+            assert accepted(s) == 7
+            if s.q_tokens < 1 << 30 and s.q_tokens * qh * hd < (1 << 40) - qh * hd and s.q_tokens == q_most:
+                s.q_tokens += 4
+                assert accepted(s) == 2
+
+
+@pytest.mark.parametrize("tokens", [1, 511, 4096, 1 << 25, 1 << 26, (1 << 31) - 1])
+@pytest.mark.parametrize("heads,hd", [(1, 64), (24, 128), (65536, 64)])
+def test_largest_launches_of_the_rotation(plans, tokens, heads, hd):
+    parts, launches, blocks = plans.rope(tokens, heads, hd)
+    assert blocks * 256 < THREADS and launches == max(1, tokens >> 25) + (tokens > 1 << 25 and tokens % (1 << 25) > 0)
+    assert 1 <= parts <= -(-heads // (512 // hd))
