@@ -50,7 +50,10 @@ typedef enum {
     PURO_ROPE_NTK = 2,     /* base * factor^(rot/(rot-2)) in place of base */
     PURO_ROPE_YARN = 3     /* f_i ((1-g)/factor + g) with g = clamp((trained f_i / 2 pi - 1) / 31, 0, 1): pairs that
                               turn more than 32 times in the trained length keep their frequency, those under one
-                              turn are stretched; table scaled by 0.1 ln(factor) + 1 */
+                              turn are stretched; table scaled by 0.1 ln(factor) + 1.  The ramp is the published one,
+                              over turns; model code that ramps over pair numbers instead, between the (rounded)
+                              numbers of the pairs that turn 32 times and once, has other frequencies in between: for
+                              weights tuned with those the caller fills the table, in the same layout */
 } puro_rope_scaling;
 
 /*
@@ -110,7 +113,8 @@ puro_status puro_qk_norm_rope(const puro_rotation *r, const uint16_t *x, int64_t
  *   cache_k  [cache_rows][k_heads][head_dim], k_stride; cache_v likewise
  *   rows     [tokens]: the cache row of each token.  A row outside 0 ..
  *            cache_rows-1 leaves both caches alone (the token's q is still
- *            written); rows that repeat leave either token's keys and values.
+ *            written).  Tokens of one call that name the same row leave an
+ *            unspecified mixture of their keys and values in it, head by head.
  */
 puro_status puro_qk_norm_rope_append(const puro_rotation *r, const uint16_t *x, int64_t x_stride, int64_t tokens,
                                      int64_t q_heads, int64_t k_heads, int64_t head_dim, const uint16_t *wq,
