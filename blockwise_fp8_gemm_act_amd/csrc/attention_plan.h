@@ -40,12 +40,12 @@ struct Order {
 // ---------------------------------------------------------------- forward
 // Both kernels' times are estimated from the average sequence and the smaller wins.  A
 // workgroup costs a fixed time and one for each 64 (128) keys it walks, and 256 of them
-// run at a time; the constants, in us, are fitted to 47 shapes of heads of 128 and 97 of
-// heads of 64, with 1 to 64 sequences, 8 to 4096 queries and up to 16384 earlier keys (97
-// shapes: on average 0.3% slower than the better kernel, 17% at worst).  Examples (many /
-// few queries' kernel), 16 and 8 heads of 128: 64 x 8 queries over 2056 keys 266 / 127 us;
-// 16 x 64 over 2112 67 / 63; 8 x 512 over 512 34 / 66; 1 x 4096 over 4096 113 / 229;
-// 1 x 512 over 16896 755 / 209.
+// run at a time; the constants, in us, are fitted to 42 shapes of heads of 128 and 104 of
+// heads of 64, with 1 to 64 sequences, 8 to 4096 queries and up to 16384 earlier keys (on
+// average 0.2% slower than the better kernel, 7% at worst).  Examples (many / few queries'
+// kernel), 16 and 8 heads of 128: 64 x 8 queries over 2056 keys 145 / 127 us; 16 x 64 over
+// 2112 49 / 63; 1 x 256 over 256 14.6 / 8.3; 8 x 512 over 512 23 / 69; 1 x 1500 over 1500
+// 37 / 49; 1 x 4096 over 4096 92 / 252; 1 x 512 over 16896 309 / 210.
 inline AttnPlan forward_plan(const puro_attention_shape &a) {
   AttnPlan p{};
   const double units = 256.0;
@@ -74,7 +74,7 @@ inline AttnPlan forward_plan(const puro_attention_shape &a) {
   if (splits > kMostSplits) splits = kMostSplits;
   if (splits < 1) splits = 1;
   const bool wide = a.head_dim == 128;
-  const double per_few = wide ? 1.5 : 0.9, per_many = wide ? 1.6 : 1.3, start_few = wide ? 4 : 3, start_many = wide ? 5 : 6;
+  const double per_few = wide ? 2.2 : 0.9, per_many = wide ? 1.25 : 1.3, start_few = wide ? 6 : 3, start_many = wide ? 7 : 6;
   const double walk_few = wf < units ? most(1) / splits : mean(1);
   const double t_few = (wf < units ? 1 : wf / units) * (start_few + per_few * walk_few / (kSplitWaves * kSplitKeys));
   // Heads that share keys share a workgroup: lower blocks see fewer keys that only some

@@ -76,3 +76,16 @@ def test_largest_launches_of_the_rotation(plans, tokens, heads, hd):
     parts, launches, blocks = plans.rope(tokens, heads, hd)
     assert blocks * 256 < THREADS and launches == max(1, tokens >> 25) + (tokens > 1 << 25 and tokens % (1 << 25) > 0)
     assert 1 <= parts <= -(-heads // (512 // hd))
+
+
+# (sequences, queries, earlier keys, query heads, key heads, head_dim, us of the kernel for many queries and of the one for few)
+TIMED = [(1, 256, 0, 16, 8, 128, 14.6, 8.3), (1, 1500, 0, 16, 8, 128, 37.2, 49.3), (16, 64, 2048, 16, 8, 128, 48.6, 63.0),
+         (1, 1024, 8192, 16, 8, 128, 171.2, 225.5), (4, 512, 0, 16, 8, 128, 20.4, 36.7), (1, 4096, 0, 16, 8, 128, 91.7, 251.6),
+         (64, 8, 2048, 16, 8, 128, 145.3, 126.8), (1, 512, 16384, 16, 8, 128, 308.6, 209.8), (1, 64, 16384, 16, 8, 128, 291.6, 46.7)]
+
+
+@pytest.mark.parametrize("case", TIMED, ids=str)
+def test_the_faster_kernel_is_chosen(plans, case):
+    n, ql, earlier, qh, kh, hd, many, few = case
+    p = plans.forward(ap.shape(qh, kh, hd, n * ql, n * (ql + earlier), n, max_k=ql + earlier))
+    assert p.few == (few < many)
