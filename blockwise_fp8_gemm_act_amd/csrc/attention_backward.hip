@@ -24,9 +24,12 @@ __device__ __forceinline__ f32x16 splat(float x) {
 }
 
 // ---------------------------------------------------------------- dq
-// Three products a pair (S, do v, dS k): bound by the matrix cores, busy 61% of the time
-// (counters, 4 x 4096 tokens, 16 and 8 heads of 128: 412 GFLOP in 352 us).  Two workgroups
-// a unit at heads of 128, whose waves fill each other's gaps; of heads of 64 four.
+// Three products a pair (S, do v, dS k): bound by the matrix cores, busy 55% of the time
+// (counters, 4 x 4096 tokens, 16 and 8 heads of 128: 412 GFLOP and the walks repeated for D
+// in 376 us; vector work 46%).  dS is one bf16 in its product with k, as it and P are below:
+// relative error of the gradients 0.0024, 0.0017 of it their own rounding; a second bf16 would
+// add a product to these three and two to the four below.  Two workgroups a unit at heads of
+// 128, whose waves fill each other's gaps; of heads of 64 four.
 //
 // A workgroup takes `pack` heads of a group by kDqRows / pack queries, as the forward
 // kernel does.  Also writes, for the kernel below, stats[0][h][row] = -lse / scale (-infinity
@@ -247,11 +250,12 @@ __global__ void __launch_bounds__(64 * kDqWaves, kHd == 64 ? 4 : 2) attn_dq_kern
 // Four products a pair (S, do v, P^T do, dS^T q).  Keys stand as columns here, so that a
 // lane owns a key, and P and dS are again operands in place.  A wave holds 32 keys and
 // values (64 registers at heads of 128) and the sums of their gradients (128), which leaves
-// two waves a SIMD; the matrix cores are busy 57% of the time (550 GFLOP in 476 us at 4 x
-// 4096 tokens, 16 and 8 heads of 128).  What it took, the whole backward call there, us:
+// two waves a SIMD; the matrix cores are busy 56% of the time (550 GFLOP in 476 to 486 us at 4
+// x 4096 tokens, 16 and 8 heads of 128).  What it took, the whole backward call there, us:
 // 1492 as first built; masks without branches, reads ahead of the products and long walks
 // first 973; copies between the products 903; starting values in the accumulators 823 to 863
-// from card to card.  One wave a SIMD with twice the registers: 1150 where this took 979.
+// from card to card (847 to 896 with D put right, above).  One wave a SIMD with twice the
+// registers: 1150 where this took 979.
 //
 // DkPlan says what a workgroup's work is.
 struct Walk {

@@ -141,10 +141,10 @@ inline DkPlan plan_dk(int64_t q_tokens, int64_t k_tokens, int64_t sequences, int
   // workgroups each, three with heads of 64), and the partials' way through memory.  The
   // constants are fitted to 112 shapes of 1 to 64 sequences of 128 to 16384 tokens: 0.8%
   // slower on average than the best number, 9% at worst.  The whole backward call, causal,
-  // 1 / 2 / 3 / 4 / 6 / 8 parts, us: 4096 tokens, 16 and 8 heads of 128: 380 / 302 / 276 /
-  // 282 / 309 / 351; 4 x 4096: 860 / 932 / 979 / 1033 / 1138 / 1263; 8 x 2048, 8 heads and 1
-  // of 128: 625 / 384 / 319 / 291 / 267 / 281; 8192, 16 and 4 of 64: 839 / 596 / 528 / 502 /
-  // 506 / 505.
+  // 1 / 2 / 3 / 4 / 6 / 8 parts, us (dq has since become 7 to 12% slower, for any number):
+  // 4096 tokens, 16 and 8 heads of 128: 380 / 302 / 276 / 282 / 309 / 351; 4 x 4096: 860 / 932 /
+  // 979 / 1033 / 1138 / 1263; 8 x 2048, 8 heads and 1 of 128: 625 / 384 / 319 / 291 / 267 / 281;
+  // 8192, 16 and 4 of 64: 839 / 596 / 528 / 502 / 506 / 505.
   const bool windowed = window > 0 && window + kDkRows < per_seq;
   const int64_t seen = windowed ? window + kDkRows : per_seq;
   const int64_t longest = (seen + kDkQueries - 1) / kDkQueries * group;
