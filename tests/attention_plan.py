@@ -62,6 +62,7 @@ def shape(qh, kh, hd, q_tokens, k_tokens, sequences=1, window=0, sinks=0, max_k=
 MANY = [(16, 8, 128, 2, [2100], [2100], 0, 0), (16, 8, 128, 2, [2100], [2100], 300, 5), (16, 8, 128, 2, [1301, 700], [1301, 1400], 0, 0),
         (24, 24, 128, 1, [2049], [2049], 0, 0), (24, 24, 128, 1, [1999], [1999], 130, 0),
         (24, 8, 128, 1, [1100, 0, 900], [1100, 70, 900], 200, 70), (16, 4, 128, 4, [2111], [2111], 0, 0), (16, 4, 128, 4, [2111], [2111], 64, 1),
+        (16, 8, 128, 2, [1500, 900], [1000, 0], 0, 0), (16, 4, 64, 4, [2000, 700], [1400, 9], 300, 2),
         (32, 32, 64, 1, [2100], [2100], 0, 0), (16, 4, 64, 4, [1027, 1500], [1027, 1500], 500, 3), (32, 16, 64, 2, [2300], [2300], 0, 0)]
 
 # The same over a cache with room left: (query heads, key heads, head_dim, heads of a workgroup, queries, keys in use, room,

@@ -1,5 +1,7 @@
 """The kernel for many queries on the GPU: each number of heads a workgroup takes, long walks, windows, caches; offsets past 32
 bits and starts out of range through every kernel.  tests/test_attention_plan.py holds the shapes to their kernel."""
+import math
+
 import pytest
 import torch
 
@@ -25,12 +27,12 @@ def starts(lengths):
     return ints([sum(lengths[:i]) for i in range(len(lengths) + 1)])
 
 
-def check_heads(q, k, v, got, seqs, window, sinks):
+def check_heads(q, k, v, got, seqs, window, sinks, scale=None):
     """Some query heads against the 64-bit form: the first and last of a workgroup and of all."""
     qh, kh = q.shape[1], k.shape[1]
     for h in sorted({0, 1, qh // 2, qh - 1}):
         g = h * kh // qh
-        want = ref.attention(q[:, h:h + 1], k[:, g:g + 1], v[:, g:g + 1], seqs, window, sinks, bounds=True)
+        want = ref.attention(q[:, h:h + 1], k[:, g:g + 1], v[:, g:g + 1], seqs, window, sinks, scale, bounds=True)
         ref.check(got[0][:, h:h + 1], want["o"], want["b_o"], "o of head %d" % h)
         ref.check(got[1][h:h + 1], want["lse"], want["b_lse"], "lse of head %d" % h)
 
@@ -41,6 +43,31 @@ def test_long_walks(case):
     q, k, v = normal((sum(ql), qh, hd), 1), normal((sum(kl), kh, hd), 2), normal((sum(kl), kh, hd), 3)
     got = puro.attention(q, k, v, starts(ql), starts(kl), window=window, sinks=sinks)
     check_heads(q, k, v, got, [(sum(ql[:i]), ql[i], sum(kl[:i]), kl[i]) for i in range(len(ql))], window, sinks)
+
+
+@pytest.mark.parametrize("case", [c for c in ap.MANY if sum(c[4]) > sum(c[5])], ids=str)
+def test_rows_that_see_nothing(case):
+    qh, kh, hd, _, ql, kl, window, sinks = case
+    q, k, v = normal((sum(ql), qh, hd), 1), normal((sum(kl), kh, hd), 2), normal((sum(kl), kh, hd), 3)
+    for i, (n, m) in enumerate(zip(ql, kl)):
+        q[sum(ql[:i]):sum(ql[:i]) + n - m] = float("nan")
+    o, lse = puro.attention(q, k, v, starts(ql), starts(kl), window=window, sinks=sinks)
+    for i, (n, m) in enumerate(zip(ql, kl)):
+        gone = slice(sum(ql[:i]), sum(ql[:i]) + n - m)
+        assert not bool(o[gone].any()) and bool((lse[:, gone] == -math.inf).all())
+        assert bool(o[gone.stop:sum(ql[:i + 1])].isfinite().all())
+
+
+@pytest.mark.parametrize("at,by", [(0, 40.0), (63, 400.0), (64, 4000.0), (1000, 400.0), (2099, 4000.0)])
+@pytest.mark.parametrize("case", [c for c in ap.MANY if c[4] == [2100] and not c[6]], ids=str)
+def test_a_score_that_outgrows_the_others(case, at, by):
+    """One key far above all before and after it, up to where exp(s - running maximum) leaves fp32."""
+    qh, kh, hd, _, ql, kl, _, _ = case
+    q, k, v = normal((ql[0], qh, hd), 16, 0.1), normal((kl[0], kh, hd), 17, 0.1), normal((kl[0], kh, hd), 18)
+    q[:, :, 0] = 1.0
+    k[at, :, 0] = by
+    got = puro.attention(q, k, v, scale=1.0)
+    check_heads(q, k, v, got, [(0, ql[0], 0, kl[0])], 0, 0, scale=1.0)
 
 
 @pytest.mark.parametrize("case", ap.MANY_CACHED, ids=str)
