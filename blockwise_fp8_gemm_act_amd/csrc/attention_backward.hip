@@ -116,8 +116,8 @@ __global__ void __launch_bounds__(64 * kDqWaves, kHd == 64 ? 4 : 2) attn_dq_kern
   // 0.0017; keys and values with a mean of three deviations 0.51 (2.3) / 0.006 (0.05) / 0.005
   // (0.02); a key that takes nearly all 1.1 (43) / 0.0016 (0.015) / 0.0015 (0.004).  The sums
   // cost 2% and a walk again in every block 40% of the backward call (4 x 4096 tokens: 842 us
-  // without, 861 with the sums, 873 with the few walks of that case, 1176 with all); a bound of
-  // 2^-7 instead takes 918.  Blocks of rows with few keys nearly always need it: they take D
+  // without, 861 with the sums, 873 with the few walks of that case, 1176 with all; heads of 64,
+  // 4 x 4096 tokens of 16 and 4 heads: 470 / 498 with the sums); a bound of 2^-7 instead takes 918.  Blocks of rows with few keys nearly always need it: they take D
   // from a walk of its own first, two products instead of three.
   bool exact = false;
   if (kt.count > 0 && (shift + row0 < 128 || (a.window > 0 && a.window + a.sinks < 128))) {

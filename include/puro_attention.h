@@ -207,6 +207,10 @@ puro_status puro_attention(const puro_attention_shape *a, const uint16_t *q, con
  * dk and dv sum over the query heads of a key head.  Rows that see nothing, and
  * keys that nothing sees, get zeros.
  *   o, lse  as puro_attention wrote them;  d_o  the gradient of o, laid out as o
+ * Products are bf16 with fp32 sums: P and dS are rounded to bf16 for theirs.  D
+ * from the rounded o is put right by the sum of the row's dS (0 for the exact D):
+ * always for dk, for dq where that sum reaches 2^-6 of the root of the squared dS;
+ * below it, it adds scale (sum dS) (sum P k) to dq.
  * Deterministic for a given shape.
  */
 puro_status puro_attention_backward(const puro_attention_shape *a, const uint16_t *d_o, const uint16_t *q,
